@@ -309,6 +309,187 @@ int mxfp4_moe_noalloc(const void* x, int64_t t, int64_t hidden, const float* rou
                       void* y, int32_t* topk_ids, float* topk_w, void* stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * The attention side of a step: norms around a block, rotary positions with
+ * the write into the KV cache, attention of the step's new tokens over the
+ * cache, and the cache's pages between steps. They sit next to the weight
+ * calls above: their bf16 inputs and outputs are mxfp4_linear's outputs and
+ * inputs. No call synchronises, and every length and page number is read on
+ * the device, so a step can be captured once in a CUDA graph and replayed
+ * while the lengths change.
+ *
+ * Paged KV cache. K and V each live in a pool of pages of page_size tokens;
+ * a page holds [kv_heads][page_size][head_dim] elements, dense, and pages
+ * lie page_stride elements apart. The block table gives the pages of each
+ * sequence in order; an entry outside [0, num_pages) stands for no page:
+ * nothing is written there, and its tokens are seen by no query.
+ */
+typedef enum {
+    MXFP4_KV_BF16 = 0,
+    MXFP4_KV_E4M3 = 1 /* element * scale of its KV head */
+} mxfp4_kv_dtype;
+
+typedef struct {
+    void* k;              /* device, 16-byte aligned; layer 0's pool */
+    void* v;              /* device, 16-byte aligned */
+    const float* k_scale; /* device float32 [kv_heads], E4M3 only; NULL = 1 */
+    const float* v_scale; /* the same for V */
+    int64_t page_stride;  /* elements between pages; 0 = kv_heads * page_size * head_dim */
+    int64_t layer_stride; /* elements between layers' pools (mxfp4_cache_copy, _accept); 0 = num_pages * page_stride */
+    int64_t num_pages;    /* pages of a layer's pool, < 2^24 */
+    int32_t layers;       /* layers that mxfp4_cache_copy and _accept work on (1 .. 1024) */
+    int32_t kv_heads;     /* 1 .. 1024 */
+    int32_t page_size;    /* tokens: a power of two, 16 .. 1024 */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t dtype;        /* mxfp4_kv_dtype */
+    int32_t reserved;     /* 0 */
+} mxfp4_kv_cache_t;
+
+/*
+ * The new tokens of a step. Request b brings rows q_start[b] .. q_start[b+1]-1
+ * of the step's token arrays (none is allowed); they are the last tokens of
+ * its sequence: new token i of n has cache index seq_lens[b] - n + i.
+ * Lengths beyond the block table's room are cut to it.
+ */
+typedef struct {
+    const int32_t* q_start;     /* device int32 [batch + 1], ascending from 0 to at most tokens */
+    const int32_t* seq_lens;    /* device int32 [batch]: tokens in the cache, the new ones included */
+    const int32_t* block_table; /* device int32 [batch][table_width], rows table_stride apart */
+    int64_t table_stride;       /* entries; 0 = table_width */
+    int32_t table_width;
+    int32_t batch;              /* requests, 1 .. 1024 */
+    int32_t tokens;             /* rows of the step's token arrays */
+    int32_t max_q;              /* most new tokens of a request (sizes the kernels; longer ones stay right) */
+    int32_t max_seq;            /* most tokens of a sequence (the same) */
+    int32_t reserved;           /* 0 */
+} mxfp4_kv_batch_t;
+
+/*
+ * Norms between two blocks, with the block's gate and the residual sum. Per
+ * token, in fp32, each output rounded once:
+ *   u = x, or N(x) * (post_weight + weight_offset) + post_bias
+ *   u = u * gate
+ *   r = residual + scale * u
+ *   y = N(r) * (weight + weight_offset) + bias       (of the unrounded r)
+ * N(z) = z / sqrt(mean(z^2) + eps); layer != 0: the same of z - mean(z).
+ *   x, residual, y, r_out   device bf16 [tokens, n]; r_out may be residual
+ *                  and y may be x (each row is read before it is written)
+ *   post_weight    device bf16 [n], or NULL for no norm of x
+ *   post_bias      device bf16 [n] or NULL (needs post_weight)
+ *   gate           device bf16, rows gate_stride elements apart (0: one row
+ *                  for every token; otherwise >= n), or NULL
+ *   weight         device bf16 [n];  bias device bf16 [n] or NULL
+ *   n              1 .. 32768; every pointer 2-byte aligned (16 bytes, with
+ *                  n and gate_stride multiples of 8, takes the wide loads)
+ */
+int mxfp4_residual_norm(const void* x, const void* residual, int64_t tokens, int64_t n, const void* post_weight,
+                        const void* post_bias, const void* gate, int64_t gate_stride, float scale,
+                        const void* weight, const void* bias, float weight_offset, float eps, int layer, void* y,
+                        void* r_out, void* stream);
+
+/*
+ * Rotary positions of a step's new tokens, and the write of their K and V
+ * into the cache (of the layer `cache` names). The first rotary_dim elements
+ * of each q and k head turn in pairs by position * inv_freq[j]: pair j is
+ * the elements (2j, 2j+1) (interleaved != 0) or (j, j + rotary_dim/2):
+ *   (a, b) -> (a cos - b sin, a sin + b cos) * factor
+ * The rest of the head, and V, pass unchanged. Angles are reduced in fp64,
+ * so long positions keep their accuracy. Stretching a model to longer
+ * contexts is a matter of inv_freq and factor.
+ *   qkv          device bf16, rows of (q_heads + 2 kv_heads) * head_dim (q,
+ *                then k, then v) qkv_stride elements apart, 16-byte aligned,
+ *                qkv_stride % 8 == 0
+ *   positions    device int32 [tokens], or NULL: the cache index
+ *   inv_freq     device float32 [rotary_dim / 2]
+ *   rotary_dim   even, 0 .. head_dim (0: nothing turns, inv_freq may be NULL)
+ *   q_out        device bf16 [tokens, q_heads, head_dim], 16-byte aligned
+ * E4M3 caches store value / scale, rounded to nearest even and saturating at
+ * 448. Rows of qkv beyond q_start[batch] are left out.
+ */
+int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const int32_t* positions,
+                      const float* inv_freq, int rotary_dim, int interleaved, float factor,
+                      const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* batch, void* q_out, void* stream);
+
+/*
+ * Attention of a step's new tokens over the paged cache, their own K and V
+ * already in it. q_heads / kv_heads query heads in a row share a KV head.
+ *   s_j = scale * q . k_j, or softcap * tanh(scale * q . k_j / softcap)
+ *   o = sum_j softmax(s)_j v_j   over the visible keys j
+ * A query at cache index c sees j <= c; with a window, j > c - window too.
+ * tree_mask replaces j <= c among the new tokens of a request: bit j of a
+ * query's word says that it sees new token j (a draft tree's ancestors and
+ * itself); what lies before the new tokens stays visible. A query that sees
+ * nothing gives 0 (lse -inf). What is not visible has no part in a result,
+ * whatever it holds (NaN and infinities included).
+ *   q          device bf16, rows of q_heads * head_dim, q_stride elements
+ *              apart, 16-byte aligned, q_stride % 8 == 0
+ *   q_heads    a multiple of kv_heads, at most 128 * kv_heads
+ *   softcap    0: none;  window 0: none
+ *   tree_mask  device uint64 [tokens] or NULL; max_q <= 64
+ *   out        device bf16 [tokens, q_heads, head_dim], 16-byte aligned;
+ *              rows of no request are not written
+ *   lse        device float32 [tokens, q_heads] or NULL: log sum_j exp(s_j)
+ *   workspace  device, at least mxfp4_attention_workspace_size() bytes,
+ *              256-byte aligned, contents on entry do not matter
+ * Scores, maxima, sums and outputs accumulate in fp32; the probabilities of
+ * a product with V are rounded to bf16 (E4M3 caches: to f16).
+ */
+size_t mxfp4_attention_workspace_size(int q_heads, const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* batch);
+int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv_cache_t* cache,
+                    const mxfp4_kv_batch_t* batch, float scale, float softcap, int window,
+                    const uint64_t* tree_mask, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * The cache's pages from one step to the next, in one call: fork, reorder,
+ * cut back, extend and free. New sequence i continues old sequence
+ * parent[i] (or begins empty: parent[i] outside [0, old_sequences)), cut to
+ * its first keep[i] tokens (keep NULL: all), and gets room for grow[i] more:
+ *   - pages that hold kept tokens are shared, as often as they are wanted;
+ *   - a partly filled page that will grow is copied first, unless every new
+ *     sequence that holds the page will write to it and this is the first of them;
+ *   - new pages are the lowest-numbered ones that no new sequence holds,
+ *     dealt in sequence order (a copy's first). Old sequences that nobody
+ *     continues are thereby freed.
+ * Where the pool runs short, later sequences get less: lens_out says what
+ * each can hold (without its copy a sequence gets no growth at all).
+ *   table       device int32 [old_sequences][table_width], rows table_stride
+ *               (0 = table_width) apart;  seq_lens device int32 [old_sequences]
+ *   parent, keep, grow   device int32 [sequences] (1 .. 65536)
+ *   table_out   device int32 [sequences][table_width], not `table`; entries
+ *               past a sequence's pages are -1
+ *   lens_out    device int32 [sequences]: kept + grown tokens
+ *   copies      device int32 [sequences][3]: source page, target page and
+ *               rows of a page to copy (mxfp4_cache_copy), or -1, -1, 0
+ *   info        device int32 [2]: pages left free; pages asked for in vain
+ *   workspace   at least mxfp4_cache_workspace_size() bytes, 256-byte
+ *               aligned, contents on entry do not matter
+ */
+size_t mxfp4_cache_workspace_size(int64_t sequences, int64_t num_pages);
+int mxfp4_cache_update(const int32_t* table, int64_t table_stride, int table_width, const int32_t* seq_lens,
+                       int old_sequences, const int32_t* parent, const int32_t* keep, const int32_t* grow,
+                       int sequences, int64_t num_pages, int page_size, int32_t* table_out, int32_t* lens_out,
+                       int32_t* copies, int32_t* info, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Copies the first rows of pages that mxfp4_cache_update lists, K and V, in
+ * every layer of the cache.   copies  device int32 [sequences][3]
+ */
+int mxfp4_cache_copy(const mxfp4_kv_cache_t* cache, const int32_t* copies, int sequences, void* stream);
+
+/*
+ * After a verify step: moves the K and V rows of the accepted draft path to
+ * the front of each request's new tokens, in every layer. Row i of the new
+ * tokens becomes row path[b][i] for i < n_accept[b]; entries outside the new
+ * tokens move nothing.
+ *   path       device int32 [batch][path_len], path_len 1 .. 64
+ *   n_accept   device int32 [batch], cut to [0, new tokens]
+ *   lens_out   device int32 [batch], not seq_lens: tokens before the step + n_accept
+ */
+int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* batch, const int32_t* path,
+                       int path_len, const int32_t* n_accept, int32_t* lens_out, void* stream);
+
+/*
  * Synchronizes `stream`, then returns MXFP4_OK, MXFP4_ERR_TIMEOUT if some
  * kernel of this library on the current device gave up a bounded wait since
  * the last call, or MXFP4_ERR_CUDA if the stream reports an error. Clears

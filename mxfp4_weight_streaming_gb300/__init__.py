@@ -9,6 +9,12 @@ C entry points (same names as the header): mxfp4_quantize, mxfp4_linear,
 mxfp4_linear_plan, mxfp4_moe, mxfp4_moe_workspace_size,
 mxfp4_last_device_status, mxfp4_strerror. Convenience wrappers: quantize,
 linear, linear_plan (host only), moe.
+
+The attention side of a step (norms, rotary positions with the cache write,
+attention over the paged KV cache, the cache's pages) is in step.py and
+available from here: KVCache, KVBatch, residual_norm, rope_frequencies,
+rope_append, attention, attention_workspace, cache_update, cache_workspace,
+cache_copy, cache_accept.
 """
 from __future__ import annotations
 
@@ -27,7 +33,9 @@ MXFP4_ERR_CUDA = 5
 MXFP4_ERR_TIMEOUT = 6
 
 EXPORTED = ["mxfp4_strerror", "mxfp4_quantize", "mxfp4_linear", "mxfp4_linear_plan", "mxfp4_moe_workspace_size",
-            "mxfp4_moe", "mxfp4_last_device_status"]
+            "mxfp4_moe", "mxfp4_last_device_status", "mxfp4_residual_norm", "mxfp4_rope_append",
+            "mxfp4_attention_workspace_size", "mxfp4_attention", "mxfp4_cache_workspace_size", "mxfp4_cache_update",
+            "mxfp4_cache_copy", "mxfp4_cache_accept"]
 
 _lib = None
 
@@ -79,6 +87,23 @@ def load() -> ctypes.CDLL:
     L.mxfp4_last_device_status.argtypes = [P]
     L.mxfp4_linear_plan.restype = I
     L.mxfp4_linear_plan.argtypes = [I64, I64, I64, I, I, ctypes.POINTER(LinearPlan)]
+    F, S = ctypes.c_float, ctypes.c_size_t
+    L.mxfp4_residual_norm.restype = I
+    L.mxfp4_residual_norm.argtypes = [P, P, I64, I64, P, P, P, I64, F, P, P, F, F, I, P, P, P]
+    L.mxfp4_rope_append.restype = I
+    L.mxfp4_rope_append.argtypes = [P, I64, I, P, P, I, I, F, P, P, P, P]
+    L.mxfp4_attention_workspace_size.restype = S
+    L.mxfp4_attention_workspace_size.argtypes = [I, P, P]
+    L.mxfp4_attention.restype = I
+    L.mxfp4_attention.argtypes = [P, I64, I, P, P, F, F, I, P, P, P, P, S, P]
+    L.mxfp4_cache_workspace_size.restype = S
+    L.mxfp4_cache_workspace_size.argtypes = [I64, I64]
+    L.mxfp4_cache_update.restype = I
+    L.mxfp4_cache_update.argtypes = [P, I64, I, P, I, P, P, P, I, I64, I, P, P, P, P, P, S, P]
+    L.mxfp4_cache_copy.restype = I
+    L.mxfp4_cache_copy.argtypes = [P, P, I, P]
+    L.mxfp4_cache_accept.restype = I
+    L.mxfp4_cache_accept.argtypes = [P, P, P, I, P, P, P]
     _lib = L
     return L
 
@@ -228,3 +253,7 @@ def linear_plan(t, k, n, num_sms=152, max_smem=232448) -> dict:
 
 def last_device_status(stream=None) -> int:
     return mxfp4_last_device_status(_stream(stream))
+
+
+from .step import (KVBatch, KVCache, attention, attention_workspace, cache_accept, cache_copy,  # noqa: E402,F401
+                   cache_update, cache_workspace, residual_norm, rope_append, rope_frequencies)

@@ -1,0 +1,168 @@
+// What the attention kernels share: how the step's work is cut, the
+// workspace of partial results, and the join of the parts.
+//
+// The rows of a KV head's queries in one request are its (token, head of the
+// group) pairs, row = token * G + head: all of them read the same K and V. A
+// row tile of R rows and its visible keys are an item; an item is cut into
+// key tiles, and the key tiles of all items of the step, counted in order
+// (request, row tile, KV head, key tile), are dealt to the CTAs in equal
+// runs. So a long sequence is shared by many CTAs and many short ones share
+// a CTA, whatever the lengths on the device are. A CTA whose run begins or
+// ends inside an item leaves that item's part in the workspace (at most two
+// per CTA); items that lie whole in a run are finished by their CTA.
+#pragma once
+
+#include "step_common.cuh"
+
+namespace mxfp4 {
+namespace attn {
+
+constexpr int kMaxBatch = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Cut of one call.
+struct Cut {
+    int group;       // query heads per KV head
+    int kv_heads;
+    int row_tile;    // R
+    int key_tile;    // keys per unit of work
+    int window;      // 0: none
+    bool tree;
+    int min_share;   // units a CTA takes at least
+};
+
+// Keys [begin, end) that some row of row tile rt of a request sees; begin is
+// rounded down to a key tile only where tiles are counted.
+__device__ __forceinline__ void item_keys(const Cut& c, int n, int seq, int rt, int& begin, int& end) {
+    const int tok0 = static_cast<int>(static_cast<int64_t>(rt) * c.row_tile / c.group);
+    const int tok1 = min(n - 1, static_cast<int>((static_cast<int64_t>(rt) * c.row_tile + c.row_tile - 1) / c.group));
+    end = c.tree ? seq : max(seq - n + tok1 + 1, 0);
+    begin = c.window ? max(seq - n + tok0 - c.window + 1, 0) : 0;
+    end = max(end, begin);
+}
+
+__device__ __forceinline__ int item_tiles(const Cut& c, int n, int seq, int rt) {
+    int begin, end;
+    item_keys(c, n, seq, rt, begin, end);
+    return max((end + c.key_tile - 1) / c.key_tile - begin / c.key_tile, 1);
+}
+
+__device__ __forceinline__ int row_tiles(const Cut& c, int n) {
+    return static_cast<int>((static_cast<int64_t>(n) * c.group + c.row_tile - 1) / c.row_tile);
+}
+
+// Units of work before each request; all threads of the block call it.
+__device__ __forceinline__ void count_units(const Cut& c, const BatchView& bt, int page_shift, int64_t* before) {
+    for (int b = threadIdx.x; b < bt.batch; b += blockDim.x) {
+        int first, n, seq;
+        request_extent(bt, b, page_shift, first, n, seq);
+        int64_t u = 0;
+        for (int rt = row_tiles(c, n) - 1; rt >= 0; --rt) u += item_tiles(c, n, seq, rt);
+        before[b + 1] = u * c.kv_heads;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int64_t carry = 0;
+        for (int b0 = 0; b0 < bt.batch; b0 += 32) {
+            const int b = b0 + threadIdx.x;
+            int64_t v = b < bt.batch ? before[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+                if (static_cast<int>(threadIdx.x) >= o) v += t;
+            }
+            v += carry;
+            if (b < bt.batch) before[b + 1] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (threadIdx.x == 0) before[0] = 0;
+    }
+    __syncthreads();
+}
+
+struct Item {
+    int b, rt, head;        // request, row tile, KV head
+    int first, n, seq;      // the request's extent
+    int begin, end;         // visible keys
+    int tile, tiles;        // the unit's key tile within the item, and the item's count
+};
+
+__device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int page_shift, const int64_t* before,
+                                       int64_t unit) {
+    Item it;
+    int lo = 0, hi = bt.batch;  // before[lo] <= unit < before[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= unit) lo = mid;
+        else hi = mid;
+    }
+    it.b = lo;
+    request_extent(bt, lo, page_shift, it.first, it.n, it.seq);
+    int64_t rem = unit - before[lo];
+    it.rt = 0;
+    while (true) {
+        it.tiles = item_tiles(c, it.n, it.seq, it.rt);
+        const int64_t block = static_cast<int64_t>(it.tiles) * c.kv_heads;
+        if (rem < block) break;
+        rem -= block;
+        ++it.rt;
+    }
+    it.head = static_cast<int>(rem / it.tiles);
+    it.tile = static_cast<int>(rem % it.tiles);
+    item_keys(c, it.n, it.seq, it.rt, it.begin, it.end);
+    return it;
+}
+
+__device__ __forceinline__ int64_t share_of(const Cut& c, int64_t total, int ctas) {
+    return max((total + ctas - 1) / ctas, static_cast<int64_t>(c.min_share));
+}
+
+// Partial results: two slots per CTA, slot 2c for a part that began before
+// the CTA's run and 2c + 1 for one that begins in it.
+struct Parts {
+    float* o;        // [2 ctas][R][D], not divided by the sum
+    float2* ml;      // [2 ctas][R]: running maximum (of log2 scores) and sum
+    int4* split;     // [ctas]: parts of the item that begins in CTA c and ends beyond it (0: none), request, row tile, KV head
+};
+
+__host__ __device__ inline size_t parts_bytes(int ctas, int rows, int d) {
+    return static_cast<size_t>(ctas) * (2 * rows * (d * sizeof(float) + sizeof(float2)) + sizeof(int4));
+}
+
+__host__ __device__ inline Parts parts_in(void* ws, int ctas, int rows, int d) {
+    Parts p;
+    p.split = static_cast<int4*>(ws);
+    p.ml = reinterpret_cast<float2*>(p.split + ctas);
+    p.o = reinterpret_cast<float*>(p.ml + static_cast<size_t>(2) * ctas * rows);
+    return p;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Scores in the log2 domain: s * scale * log2(e), or with a cap
+// cap * tanh(s * scale / cap) * log2(e). tanh x = 1 - 2 / (1 + e^2x): off by
+// a few 1e-7 of the cap (the hardware's tanh, off by 5e-4 of it, would cost
+// percents of a probability).
+struct ScoreMap {
+    float mul;      // scale * log2(e), or 2 * scale / cap * log2(e)
+    float cap;      // cap * log2(e); 0: no cap
+    __device__ __forceinline__ float operator()(float s) const {
+        if (cap == 0.f) return s * mul;
+        const float e = exp2_fast(fminf(s * mul, 80.f));
+        return cap - __fdividef(2.f * cap, 1.f + e);
+    }
+};
+
+inline ScoreMap score_map(float scale, float softcap) {
+    ScoreMap m;
+    m.cap = softcap > 0.f ? softcap * kLog2e : 0.f;
+    m.mul = softcap > 0.f ? 2.f * scale / softcap * kLog2e : scale * kLog2e;
+    return m;
+}
+
+}  // namespace attn
+}  // namespace mxfp4

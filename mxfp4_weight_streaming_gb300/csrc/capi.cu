@@ -14,6 +14,7 @@
 #include "moe_launch.h"
 #include "tc_linear_launch.h"
 #include "f4_linear_launch.h"
+#include "step_common.cuh"
 #include "mxfp4.h"
 
 namespace {
@@ -131,6 +132,15 @@ int encode_f4_weight_map(CUtensorMap* map, const uint8_t* wq, int64_t rows, int6
 }  // namespace
 
 namespace mxfp4 {
+int device_caps(DeviceCaps* out) {
+    DeviceInfo* d = nullptr;
+    if (int rc = device_info(&d)) return rc;
+    out->num_sms = d->num_sms;
+    out->max_smem = d->max_smem;
+    out->status = d->status;
+    return MXFP4_OK;
+}
+
 int encode_weights(CUtensorMap* map, const uint8_t* wq, int64_t rows, int64_t k, int steps, int* is3d) {
     return encode_weight_map(map, wq, rows, k, steps, is3d);
 }
