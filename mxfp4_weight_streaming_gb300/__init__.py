@@ -255,5 +255,14 @@ def last_device_status(stream=None) -> int:
     return mxfp4_last_device_status(_stream(stream))
 
 
-from .step import (KVBatch, KVCache, attention, attention_workspace, cache_accept, cache_copy,  # noqa: E402,F401
-                   cache_update, cache_workspace, residual_norm, rope_append, rope_frequencies)
+_STEP = ("KVBatch", "KVCache", "attention", "attention_workspace", "cache_accept", "cache_copy", "cache_update",
+         "cache_workspace", "residual_norm", "rope_append", "rope_frequencies")
+
+
+def __getattr__(name):
+    """step.py needs torch, which the rest of this module imports only when called: it is read at first use."""
+    if name not in _STEP:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import step
+    globals().update((n, getattr(step, n)) for n in _STEP)
+    return globals()[name]

@@ -13,7 +13,13 @@ from __future__ import annotations
 import ctypes
 import math
 
+import torch
+
 KV_BF16, KV_E4M3 = 0, 1
+
+_BF16, _E4M3, _F32, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
+_empty = torch.empty
+_L = None  # the loaded library, from the first call on
 
 
 class KVCacheStruct(ctypes.Structure):
@@ -30,15 +36,25 @@ class KVBatchStruct(ctypes.Structure):
         [(n, ctypes.c_int32) for n in ("table_width", "batch", "tokens", "max_q", "max_seq", "reserved")]
 
 
+# A small call spends more time on the host than on the GPU, so what every
+# call does here is kept short: the library is looked up once, checks are
+# plain attribute reads, and the current stream is read as a raw handle (0.1
+# us; torch.cuda.current_stream() makes an object in 2.9 us).
 def _lib():
-    from . import load
-    return load()
+    global _L
+    if _L is None:
+        from . import load
+        _L = load()
+    return _L
 
 
-def _check(rc: int, what: str):
-    if rc:
-        from . import Mxfp4Error
-        raise Mxfp4Error(rc, what)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _fail(rc: int, what: str):
+    from . import Mxfp4Error
+    raise Mxfp4Error(rc, what)
 
 
 def _need(ok, what: str):
@@ -50,23 +66,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _int32(t, shape, name):
-    import torch
-    _need(t.is_cuda and t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{name}: contiguous int32 CUDA tensor {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+def _ints(t, count, name):
+    """An int32 vector or matrix the C side can take as it lies in memory."""
+    if t.dtype is not _I32 or t.numel() != count or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 CUDA tensor of {count} expected, got {t.dtype} {list(t.shape)}")
 
 
 def _stream_of(stream, *made):
-    """The raw stream to launch on. Tensors made for the call are kept for a
-    stream that is not torch's current one until its work is done."""
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    """The raw handle of a stream given by the caller. Tensors made for the
+    call are kept until that stream's work on them is done."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     for t in made:
-        if t is not None:
-            t.record_stream(stream)
+        t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -78,7 +90,6 @@ class KVCache:
     one layer: `cache.layer(i)`."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
         _need(k.dim() in (4, 5) and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
               "k and v: pools of one shape, type and strides expected")
         _need(k.is_cuda and v.is_cuda and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
@@ -110,10 +121,9 @@ class KVBatch:
     rows of the token arrays and bounds of a request's new tokens and length."""
 
     def __init__(self, q_start, seq_lens, block_table, tokens, max_q, max_seq):
-        import torch
         b = seq_lens.numel()
-        _int32(seq_lens, (b,), "seq_lens")
-        _int32(q_start, (b + 1,), "q_start")
+        _ints(seq_lens, b, "seq_lens")
+        _ints(q_start, b + 1, "q_start")
         _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2
               and block_table.shape[0] == b and block_table.stride(1) == 1,
               "block_table: int32 CUDA tensor [batch, width] expected")
@@ -131,30 +141,34 @@ def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=No
     """(y, r) of bf16 [tokens, n] x and residual: r = residual + scale * gate * u
     with u = x or norm(x) * post_weight + post_bias, and y = norm(r) * weight + bias.
     gate: [n] or [tokens, n]; kind "rms" or "layer"; weights count as weight + weight_offset."""
-    import torch
-    _need(kind in ("rms", "layer"), "kind: 'rms' or 'layer' expected")
-    bf = torch.bfloat16
-    _need(x.dim() == 2 and x.is_cuda and x.dtype == bf and x.is_contiguous() and residual.shape == x.shape
-          and residual.dtype == bf and residual.is_contiguous(), "x and residual: contiguous bf16 [tokens, n] expected")
-    t, n = x.shape
+    shape = x.shape
+    if len(shape) != 2 or x.dtype is not _BF16 or residual.dtype is not _BF16 or residual.shape != shape or \
+            not x.is_cuda or not x.is_contiguous() or not residual.is_contiguous():
+        raise ValueError("x and residual: contiguous bf16 CUDA tensors [tokens, n] expected")
+    t, n = shape
     for w in (weight, post_weight, post_bias, bias):
-        _need(w is None or (w.dtype == bf and w.shape == (n,) and w.is_contiguous()), "weights: bf16 [n] expected")
+        if w is not None and (w.dtype is not _BF16 or w.numel() != n or not w.is_contiguous()):
+            raise ValueError("weights: contiguous bf16 [n] expected")
     gate_stride = 0
     if gate is not None:
-        _need(gate.dtype == bf and gate.shape in ((n,), (t, n)) and gate.stride(-1) == 1,
+        _need(gate.dtype is _BF16 and gate.shape in ((n,), (t, n)) and gate.stride(-1) == 1,
               "gate: bf16 [n] or [tokens, n] expected")
         if gate.dim() == 2:
-            gate_stride = gate.stride(0)
+            gate_stride = gate.stride(0) if t > 1 else n
     for o in (out, residual_out):
-        _need(o is None or (o.dtype == bf and o.shape == x.shape and o.is_contiguous()),
-              "outputs: contiguous bf16 [tokens, n] expected")
+        if o is not None and (o.dtype is not _BF16 or o.shape != shape or not o.is_contiguous()):
+            raise ValueError("outputs: contiguous bf16 [tokens, n] expected")
+    if kind != "rms" and kind != "layer":
+        raise ValueError("kind: 'rms' or 'layer' expected")
     y = torch.empty_like(x) if out is None else out
     r = torch.empty_like(x) if residual_out is None else residual_out
-    _check(_lib().mxfp4_residual_norm(x.data_ptr(), residual.data_ptr(), t, n, _ptr(post_weight), _ptr(post_bias),
-                                      _ptr(gate), gate_stride, scale, weight.data_ptr(), _ptr(bias), weight_offset,
-                                      eps, kind == "layer", y.data_ptr(), r.data_ptr(),
-                                      _stream_of(stream, None if out is not None else y,
-                                                 None if residual_out is not None else r)), "mxfp4_residual_norm")
+    raw = _raw_stream(x.get_device()) if stream is None else _stream_of(stream, y, r)
+    rc = (_L or _lib()).mxfp4_residual_norm(
+        x.data_ptr(), residual.data_ptr(), t, n, None if post_weight is None else post_weight.data_ptr(),
+        _ptr(post_bias), _ptr(gate), gate_stride, scale, weight.data_ptr(), _ptr(bias), weight_offset, eps,
+        kind == "layer", y.data_ptr(), r.data_ptr(), raw)
+    if rc:
+        _fail(rc, "mxfp4_residual_norm")
     return y, r
 
 
@@ -172,7 +186,6 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
                 divided by factor, a linear ramp (over the pair's index)
                 between; q and k are scaled by 0.1 ln(factor) + 1.
     """
-    import torch
     _need(rotary_dim >= 2 and rotary_dim % 2 == 0 and factor > 0, "rotary_dim: even, factor: positive expected")
     _need(scaling in (None, "linear", "base", "ramp"), "scaling: None, 'linear', 'base' or 'ramp' expected")
     half = rotary_dim // 2
@@ -202,30 +215,36 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
     head_dim], q then k then v) by their positions, writes k and v to the
     cache and returns q, bf16 [tokens, q_heads, head_dim]. inv_freq float32
     [rotary_dim / 2] (None: only the cache write)."""
-    import torch
-    d = cache.head_dim
-    _need(qkv.is_cuda and qkv.dtype == torch.bfloat16 and qkv.dim() == 2 and qkv.stride(1) == 1
-          and tuple(qkv.shape) == (batch.tokens, (q_heads + 2 * cache.kv_heads) * d),
-          "qkv: bf16 [tokens, (q_heads + 2 kv_heads) * head_dim] expected")
-    _need(inv_freq is None or (inv_freq.is_cuda and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()
-                               and inv_freq.dim() == 1), "inv_freq: float32 [rotary_dim / 2] expected")
+    tokens, d = batch.tokens, cache.head_dim
+    if qkv.dtype is not _BF16 or qkv.shape != (tokens, (q_heads + 2 * cache.kv_heads) * d) or not qkv.is_cuda or \
+            qkv.stride(1) != 1:
+        raise ValueError("qkv: bf16 CUDA tensor [tokens, (q_heads + 2 kv_heads) * head_dim] expected")
+    rotary = 0
+    if inv_freq is not None:
+        if inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
+            raise ValueError("inv_freq: float32 CUDA tensor [rotary_dim / 2] expected")
+        rotary = 2 * inv_freq.numel()
     if positions is not None:
-        _int32(positions, (batch.tokens,), "positions")
-    _need(out is None or (out.dtype == torch.bfloat16 and out.shape == (batch.tokens, q_heads, d)
-                          and out.is_contiguous()), "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
-    q = torch.empty((batch.tokens, q_heads, d), dtype=torch.bfloat16, device=qkv.device) if out is None else out
-    _check(_lib().mxfp4_rope_append(qkv.data_ptr(), qkv.stride(0), q_heads, _ptr(positions), _ptr(inv_freq),
-                                    0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, factor, cache.ref,
-                                    batch.ref, q.data_ptr(), _stream_of(stream, None if out is not None else q)),
-           "mxfp4_rope_append")
+        _ints(positions, tokens, "positions")
+    if out is None:
+        q = _empty((tokens, q_heads, d), dtype=_BF16, device=qkv.device)
+    else:
+        _need(out.dtype is _BF16 and out.shape == (tokens, q_heads, d) and out.is_contiguous(),
+              "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
+        q = out
+    raw = _raw_stream(qkv.get_device()) if stream is None else _stream_of(stream, q)
+    rc = (_L or _lib()).mxfp4_rope_append(
+        qkv.data_ptr(), qkv.stride(0), q_heads, _ptr(positions), _ptr(inv_freq), rotary, interleaved, factor,
+        cache.ref, batch.ref, q.data_ptr(), raw)
+    if rc:
+        _fail(rc, "mxfp4_rope_append")
     return q
 
 
 def attention_workspace(q_heads, cache, batch):
     """Scratch for attention calls with this cache and batch (any lengths)."""
-    import torch
     nbytes = _lib().mxfp4_attention_workspace_size(q_heads, cache.ref, batch.ref)
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=cache.k.device)
+    return _empty(max(nbytes, 256), dtype=torch.uint8, device=cache.k.device)
 
 
 def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None, out=None, lse=None, workspace=None,
@@ -233,32 +252,37 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
     """bf16 [tokens, q_heads, head_dim]: attention of q (same shape, rows may
     be strided) over the cache. scale defaults to head_dim ** -0.5; tree_mask
     int64 [tokens] (bit j: sees new token j); lse: float32 [tokens, q_heads] output."""
-    import torch
-    d = cache.head_dim
-    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[0] == batch.tokens
-          and q.shape[2] == d and q.stride(2) == 1 and q.stride(1) == d,
-          "q: bf16 [tokens, q_heads, head_dim] with dense rows expected")
-    heads = q.shape[1]
-    _need(tree_mask is None or (tree_mask.dtype == torch.int64 and tree_mask.shape == (batch.tokens,)
-                                and tree_mask.is_contiguous()), "tree_mask: int64 [tokens] expected")
-    _need(out is None or (out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous()),
-          "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == q.shape[:2] and lse.is_contiguous()),
-          "lse: contiguous float32 [tokens, q_heads] expected")
-    o = torch.empty((batch.tokens, heads, d), dtype=torch.bfloat16, device=q.device) if out is None else out
+    tokens, heads, d = shape = q.shape
+    if q.dtype is not _BF16 or tokens != batch.tokens or d != cache.head_dim or not q.is_cuda:
+        raise ValueError("q: bf16 CUDA tensor [tokens, q_heads, head_dim] expected")
+    stride, head_stride, one = q.stride()
+    _need(one == 1 and (head_stride == d or heads == 1), "q: dense rows expected")
+    if tree_mask is not None:
+        _need(tree_mask.dtype is _I64 and tree_mask.shape == (tokens,) and tree_mask.is_contiguous(),
+              "tree_mask: int64 [tokens] expected")
+    if out is None:
+        o = _empty(shape, dtype=_BF16, device=q.device)
+    else:
+        _need(out.dtype is _BF16 and out.shape == shape and out.is_contiguous(),
+              "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
+        o = out
+    if lse is not None:
+        _need(lse.dtype is _F32 and lse.shape == shape[:2] and lse.is_contiguous(),
+              "lse: contiguous float32 [tokens, q_heads] expected")
     ws = attention_workspace(heads, cache, batch) if workspace is None else workspace
-    _check(_lib().mxfp4_attention(q.data_ptr(), q.stride(0) if batch.tokens > 1 else heads * d, heads, cache.ref,
-                                  batch.ref, d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask),
-                                  o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                                  _stream_of(stream, None if out is not None else o,
-                                             None if workspace is not None else ws)), "mxfp4_attention")
+    raw = _raw_stream(q.get_device()) if stream is None else _stream_of(stream, o, ws)
+    rc = (_L or _lib()).mxfp4_attention(
+        q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
+        d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), o.data_ptr(), _ptr(lse),
+        ws.data_ptr(), ws.nbytes, raw)
+    if rc:
+        _fail(rc, "mxfp4_attention")
     return o
 
 
 def cache_workspace(sequences, num_pages, device="cuda"):
     """Scratch for cache_update calls of up to these sizes."""
-    import torch
-    return torch.empty(_lib().mxfp4_cache_workspace_size(sequences, num_pages), dtype=torch.uint8, device=device)
+    return _empty(_lib().mxfp4_cache_workspace_size(sequences, num_pages), dtype=torch.uint8, device=device)
 
 
 def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=None, stream=None):
@@ -267,48 +291,55 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     all), with room for grow[i] more. Returns (block_table, seq_lens, copies,
     info): int32 [n, width], [n], [n, 3] for cache_copy, and [pages left
     free, pages asked for in vain]."""
-    import torch
     n, old = parent.numel(), seq_lens.numel()
-    _int32(parent, (n,), "parent")
-    _int32(grow, (n,), "grow")
-    _int32(seq_lens, (old,), "seq_lens")
+    _ints(parent, n, "parent")
+    _ints(grow, n, "grow")
+    _ints(seq_lens, old, "seq_lens")
     if keep is not None:
-        _int32(keep, (n,), "keep")
-    _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2
-          and block_table.shape[0] == old and block_table.stride(1) == 1, "block_table: int32 [old, width] expected")
+        _ints(keep, n, "keep")
+    if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.shape[0] != old or \
+            block_table.stride(1) != 1 or not block_table.is_cuda:
+        raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
     width = block_table.shape[1]
-    dev = block_table.device
-    made = torch.empty(n * (width + 4) + 2, dtype=torch.int32, device=dev)  # one allocation for the four outputs
+    made = _empty(n * (width + 4) + 2, dtype=_I32, device=block_table.device)  # one allocation for the four outputs
     table, lens, copies, info = made.split((n * width, n, 3 * n, 2))
-    table, copies = table.view(n, width), copies.view(n, 3)
-    ws = cache_workspace(n, cache.num_pages, dev) if workspace is None else workspace
-    _check(_lib().mxfp4_cache_update(block_table.data_ptr(), block_table.stride(0) if old > 1 else width, width,
-                                     seq_lens.data_ptr(), old, parent.data_ptr(), _ptr(keep), grow.data_ptr(), n,
-                                     cache.num_pages, cache.page_size, table.data_ptr(), lens.data_ptr(),
-                                     copies.data_ptr(), info.data_ptr(), ws.data_ptr(), ws.numel(),
-                                     _stream_of(stream, made, None if workspace is not None else ws)),
-           "mxfp4_cache_update")
-    return table, lens, copies, info
+    ws = cache_workspace(n, cache.num_pages, made.device) if workspace is None else workspace
+    raw = _raw_stream(made.get_device()) if stream is None else _stream_of(stream, made, ws)
+    at = made.data_ptr()
+    rc = (_L or _lib()).mxfp4_cache_update(
+        block_table.data_ptr(), block_table.stride(0) if old > 1 else width, width, seq_lens.data_ptr(), old,
+        parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, at, at + 4 * n * width,
+        at + 4 * n * (width + 1), at + 4 * n * (width + 4), ws.data_ptr(), ws.nbytes, raw)
+    if rc:
+        _fail(rc, "mxfp4_cache_update")
+    return table.view(n, width), lens, copies.view(n, 3), info
 
 
 def cache_copy(cache, copies, stream=None):
     """Copies the page rows that cache_update lists, in every layer of the cache."""
-    _int32(copies, (copies.shape[0], 3), "copies")
-    _check(_lib().mxfp4_cache_copy(cache.ref, copies.data_ptr(), copies.shape[0], _stream_of(stream)),
-           "mxfp4_cache_copy")
+    n = copies.shape[0]
+    _ints(copies, 3 * n, "copies")
+    raw = _raw_stream(copies.get_device()) if stream is None else _stream_of(stream)
+    rc = (_L or _lib()).mxfp4_cache_copy(cache.ref, copies.data_ptr(), n, raw)
+    if rc:
+        _fail(rc, "mxfp4_cache_copy")
 
 
 def cache_accept(cache, batch, path, n_accept, out=None, stream=None):
     """Moves the rows of the accepted path (int32 [batch, path_len], indices
     among a request's new tokens; n_accept int32 [batch]) to the front of its
     new tokens, in every layer. Returns the lengths with the accepted tokens, int32 [batch]."""
-    import torch
-    _int32(path, (batch.batch, path.shape[1]), "path")
-    _int32(n_accept, (batch.batch,), "n_accept")
-    if out is not None:
-        _int32(out, (batch.batch,), "out")
-    lens = torch.empty(batch.batch, dtype=torch.int32, device=path.device) if out is None else out
-    _check(_lib().mxfp4_cache_accept(cache.ref, batch.ref, path.data_ptr(), path.shape[1], n_accept.data_ptr(),
-                                     lens.data_ptr(), _stream_of(stream, None if out is not None else lens)),
-           "mxfp4_cache_accept")
+    n, length = batch.batch, path.shape[1]
+    _ints(path, n * length, "path")
+    _ints(n_accept, n, "n_accept")
+    if out is None:
+        lens = _empty(n, dtype=_I32, device=path.device)
+    else:
+        _ints(out, n, "out")
+        lens = out
+    raw = _raw_stream(path.get_device()) if stream is None else _stream_of(stream, lens)
+    rc = (_L or _lib()).mxfp4_cache_accept(cache.ref, batch.ref, path.data_ptr(), length, n_accept.data_ptr(),
+                                           lens.data_ptr(), raw)
+    if rc:
+        _fail(rc, "mxfp4_cache_accept")
     return lens
