@@ -322,7 +322,7 @@ int mxfp4_moe_noalloc(const void* x, int64_t t, int64_t hidden, const float* rou
  * a page holds [kv_heads][page_size][head_dim] elements, dense, and pages
  * lie page_stride elements apart. The block table gives the pages of each
  * sequence in order; an entry outside [0, num_pages) stands for no page:
- * nothing is written there, and its tokens are seen by no query.
+ * nothing is written there, and it reads as rows of zeros.
  */
 typedef enum {
     MXFP4_KV_BF16 = 0,

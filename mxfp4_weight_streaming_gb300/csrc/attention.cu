@@ -34,20 +34,6 @@ constexpr int kCtasPerSm = 2;
 // rescaled.
 constexpr float kSlack = 8.f;
 
-struct Params {
-    const __nv_bfloat16* q;
-    int64_t q_stride;
-    const unsigned long long* tree_mask;
-    __nv_bfloat16* out;
-    float* lse;
-    void* ws;
-    int q_heads;
-    ScoreMap map;
-    Cut cut;
-    CacheView cache;
-    BatchView batch;
-};
-
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
                                                   uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -141,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     static_assert(STAGES >= 3 && R * D * 4 <= STAGES * STAGE, "ring too small for the join");
 
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_before[kMaxBatch + 1];
+    __shared__ int64_t s_before[kGroups + 1];
     __shared__ float s_m[kWarps][R], s_l[kWarps][R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -154,8 +140,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     const Parts parts = parts_in(p.ws, gridDim.x, R, D);
 
     pdl_wait_previous();
-    count_units(cut, p.batch, cv.page_shift, s_before);
-    const int64_t total = s_before[p.batch.batch];
+    const int64_t total = count_units(cut, p.batch, cv.page_shift, s_before);
     const int64_t share = share_of(cut, total, gridDim.x);
     int64_t unit = share * blockIdx.x;
     const int64_t unit_end = min(unit + share, total);
@@ -597,9 +582,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
     }
     PdlLaunch l(dim3(ctas), dim3(kThreads), smem, stream);
     e = cudaLaunchKernelEx(&l.cfg, attention_rows_kernel<D, E4M3, MT>, p);
-    if (e != cudaSuccess) return e;
-    PdlLaunch j(dim3(ctas, 16 * MT / kWarps), dim3(kThreads), 0, stream);
-    return cudaLaunchKernelEx(&j.cfg, attention_join_kernel<D, E4M3>, p, ctas);
+    return e == cudaSuccess ? launch_join(p, E4M3, ctas, stream) : e;
 }
 
 template <int D>
@@ -608,11 +591,26 @@ cudaError_t launch_d(const Params& p, bool e4m3, int mt, int ctas, cudaStream_t 
     return e4m3 ? launch<D, true, 2>(p, ctas, stream) : launch<D, false, 2>(p, ctas, stream);
 }
 
+// The tensor-core kernel where the rows of a KV head fill enough of its
+// 128-row tiles.
+bool use_tc(int64_t rows, bool e4m3) { return !e4m3 && rows > 32; }
+
 }  // namespace
+
+cudaError_t launch_join(const Params& p, bool e4m3, int ctas, cudaStream_t stream) {
+    PdlLaunch j(dim3(ctas, p.cut.row_tile / kWarps), dim3(kThreads), 0, stream);
+    if (p.cache.head_dim == 64)
+        return e4m3 ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, true>, p, ctas)
+                    : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, false>, p, ctas);
+    return e4m3 ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<128, true>, p, ctas)
+                : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<128, false>, p, ctas);
+}
+
 }  // namespace attn
 
-size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms) {
+size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, bool e4m3, int num_sms) {
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
+    if (attn::use_tc(rows, e4m3)) return attn::tc_workspace_bytes(rows, head_dim, num_sms);
     return attn::parts_bytes(attn::kCtasPerSm * num_sms, rows <= 16 ? 16 : 32, head_dim);
 }
 
@@ -625,18 +623,26 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
     p.ws = a.workspace;
+    p.status = a.status;
     p.q_heads = a.q_heads;
-    p.map = attn::score_map(a.scale, a.softcap);
     p.cut.group = a.q_heads / cache.kv_heads;
     p.cut.kv_heads = cache.kv_heads;
-    const int mt = static_cast<int64_t>(a.max_q) * p.cut.group <= 16 ? 1 : 2;
-    p.cut.row_tile = 16 * mt;
-    p.cut.key_tile = attn::kKeyTile;
     p.cut.window = a.window;
     p.cut.tree = a.tree_mask != nullptr;
     p.cut.min_share = 1;
     p.cache = cache;
     p.batch = batch;
+    const int64_t rows = static_cast<int64_t>(a.max_q) * p.cut.group;
+    if (attn::use_tc(rows, a.e4m3)) {
+        p.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
+        // Masked scores are -inf and are multiplied by `mul`: it may not be 0.
+        p.map = attn::score_map(fmaxf(fabsf(a.scale), 1e-36f), a.softcap);
+        return attn::launch_tc(p, rows, num_sms, stream);
+    }
+    p.map = attn::score_map(a.scale, a.softcap);
+    const int mt = rows <= 16 ? 1 : 2;
+    p.cut.row_tile = 16 * mt;
+    p.cut.key_tile = attn::kKeyTile;
     const int ctas = attn::kCtasPerSm * num_sms;
     return cache.head_dim == 64 ? attn::launch_d<64>(p, a.e4m3, mt, ctas, stream)
                                 : attn::launch_d<128>(p, a.e4m3, mt, ctas, stream);

@@ -17,7 +17,9 @@
 namespace mxfp4 {
 namespace attn {
 
-constexpr int kMaxBatch = 1024;
+// Requests are counted in at most this many groups of neighbours (one request
+// each up to that many), so the sums fit beside full-size tiles.
+constexpr int kGroups = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Cut of one call.
@@ -51,33 +53,44 @@ __device__ __forceinline__ int row_tiles(const Cut& c, int n) {
     return static_cast<int>((static_cast<int64_t>(n) * c.group + c.row_tile - 1) / c.row_tile);
 }
 
-// Units of work before each request; all threads of the block call it.
-__device__ __forceinline__ void count_units(const Cut& c, const BatchView& bt, int page_shift, int64_t* before) {
-    for (int b = threadIdx.x; b < bt.batch; b += blockDim.x) {
-        int first, n, seq;
-        request_extent(bt, b, page_shift, first, n, seq);
+__device__ __forceinline__ int64_t request_units(const Cut& c, const BatchView& bt, int page_shift, int b) {
+    int first, n, seq;
+    request_extent(bt, b, page_shift, first, n, seq);
+    int64_t u = 0;
+    for (int rt = row_tiles(c, n) - 1; rt >= 0; --rt) u += item_tiles(c, n, seq, rt);
+    return u * c.kv_heads;
+}
+
+__device__ __forceinline__ int requests_per_group(const BatchView& bt) { return (bt.batch + kGroups - 1) / kGroups; }
+
+// Units of work before each group of requests, and in all (before[groups]);
+// all threads of the block call it.
+__device__ __forceinline__ int64_t count_units(const Cut& c, const BatchView& bt, int page_shift, int64_t* before) {
+    const int per = requests_per_group(bt), groups = (bt.batch + per - 1) / per;
+    for (int i = threadIdx.x; i < groups; i += blockDim.x) {
         int64_t u = 0;
-        for (int rt = row_tiles(c, n) - 1; rt >= 0; --rt) u += item_tiles(c, n, seq, rt);
-        before[b + 1] = u * c.kv_heads;
+        for (int b = i * per; b < min((i + 1) * per, bt.batch); ++b) u += request_units(c, bt, page_shift, b);
+        before[i + 1] = u;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
         int64_t carry = 0;
-        for (int b0 = 0; b0 < bt.batch; b0 += 32) {
-            const int b = b0 + threadIdx.x;
-            int64_t v = b < bt.batch ? before[b + 1] : 0;
+        for (int i0 = 0; i0 < groups; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            int64_t v = i < groups ? before[i + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
                 if (static_cast<int>(threadIdx.x) >= o) v += t;
             }
             v += carry;
-            if (b < bt.batch) before[b + 1] = v;
+            if (i < groups) before[i + 1] = v;
             carry = __shfl_sync(0xffffffffu, v, 31);
         }
         if (threadIdx.x == 0) before[0] = 0;
     }
     __syncthreads();
+    return before[groups];
 }
 
 struct Item {
@@ -90,15 +103,18 @@ struct Item {
 __device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int page_shift, const int64_t* before,
                                        int64_t unit) {
     Item it;
-    int lo = 0, hi = bt.batch;  // before[lo] <= unit < before[hi]
+    const int per = requests_per_group(bt);
+    int lo = 0, hi = (bt.batch + per - 1) / per;  // before[lo] <= unit < before[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (before[mid] <= unit) lo = mid;
         else hi = mid;
     }
-    it.b = lo;
-    request_extent(bt, lo, page_shift, it.first, it.n, it.seq);
     int64_t rem = unit - before[lo];
+    it.b = lo * per;
+    if (per > 1)
+        for (int64_t u; rem >= (u = request_units(c, bt, page_shift, it.b)); ++it.b) rem -= u;
+    request_extent(bt, it.b, page_shift, it.first, it.n, it.seq);
     it.rt = 0;
     while (true) {
         it.tiles = item_tiles(c, it.n, it.seq, it.rt);
@@ -156,6 +172,30 @@ struct ScoreMap {
         return cap - __fdividef(2.f * cap, 1.f + e);
     }
 };
+
+// What the kernels take.
+struct Params {
+    const __nv_bfloat16* q;
+    int64_t q_stride;
+    const unsigned long long* tree_mask;
+    __nv_bfloat16* out;
+    float* lse;
+    void* ws;
+    unsigned* status;
+    int q_heads;
+    uint32_t q_flip;  // attention_tc.cu: sign bits to flip in q (a negative scale)
+    ScoreMap map;
+    Cut cut;
+    CacheView cache;
+    BatchView batch;
+};
+
+// Joins the parts that `ctas` CTAs left in the workspace (attention.cu).
+cudaError_t launch_join(const Params& p, bool e4m3, int ctas, cudaStream_t stream);
+
+// The tensor-core kernel (attention_tc.cu): bf16 caches, any number of rows.
+size_t tc_workspace_bytes(int64_t rows, int d, int num_sms);
+cudaError_t launch_tc(const Params& p, int64_t rows, int num_sms, cudaStream_t stream);
 
 inline ScoreMap score_map(float scale, float softcap) {
     ScoreMap m;

@@ -15,6 +15,7 @@
 #include "tc_linear_launch.h"
 #include "f4_linear_launch.h"
 #include "step_common.cuh"
+#include "step_launch.h"
 #include "mxfp4.h"
 
 namespace {
@@ -139,6 +140,18 @@ int device_caps(DeviceCaps* out) {
     out->max_smem = d->max_smem;
     out->status = d->status;
     return MXFP4_OK;
+}
+
+cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& c) {
+    const cuuint64_t page = cuuint64_t(1) << c.page_shift, d = c.head_dim;
+    const cuuint64_t dims[4] = {d, page, static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[3] = {d * 2, page * d * 2, static_cast<cuuint64_t>(c.page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box,
+                                estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 int encode_weights(CUtensorMap* map, const uint8_t* wq, int64_t rows, int64_t k, int steps, int* is3d) {

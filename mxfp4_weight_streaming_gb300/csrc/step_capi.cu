@@ -167,7 +167,8 @@ size_t mxfp4_attention_workspace_size(int q_heads, const mxfp4_kv_cache_t* cache
         return 0;
     mxfp4::DeviceCaps caps;
     const int sms = mxfp4::device_caps(&caps) == MXFP4_OK ? caps.num_sms : 152;
-    return mxfp4::attention_workspace_bytes(q_heads, cache->kv_heads, cache->head_dim, batch->max_q, sms);
+    return mxfp4::attention_workspace_bytes(q_heads, cache->kv_heads, cache->head_dim, batch->max_q,
+                                             cache->dtype == MXFP4_KV_E4M3, sms);
 }
 
 int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv_cache_t* cache,
@@ -195,6 +196,7 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
     a.out = out;
     a.lse = lse;
     a.workspace = workspace;
+    a.status = caps.status;
     a.q_heads = q_heads;
     a.max_q = batch->max_q;
     a.max_seq = batch->max_seq;

@@ -2,6 +2,7 @@
 // attention.cu, kv_cache.cu). Arguments are checked by step_capi.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -39,13 +40,18 @@ struct AttentionArgs {
     void* out;   // bf16 [tokens, q_heads, head_dim]
     float* lse;  // null or [tokens, q_heads]
     void* workspace;
+    unsigned* status;
     int q_heads;
     int max_q, max_seq;
     bool e4m3;
     float scale, softcap;
     int window;
 };
-size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, int num_sms);
+size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, bool e4m3, int num_sms);
+// K or V pool of a layer as the tensor map attention_tc.cu copies from: (D,
+// page, kv_heads, pages), boxes of 64 elements x min(page, 128) tokens,
+// 128-byte swizzle (capi.cu).
+cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& cache);
 cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, const BatchView& batch, int num_sms,
                              cudaStream_t stream);
 

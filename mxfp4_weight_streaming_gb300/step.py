@@ -301,18 +301,21 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
             block_table.stride(1) != 1 or not block_table.is_cuda:
         raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
     width = block_table.shape[1]
-    made = _empty(n * (width + 4) + 2, dtype=_I32, device=block_table.device)  # one allocation for the four outputs
-    table, lens, copies, info = made.split((n * width, n, 3 * n, 2))
-    ws = cache_workspace(n, cache.num_pages, made.device) if workspace is None else workspace
-    raw = _raw_stream(made.get_device()) if stream is None else _stream_of(stream, made, ws)
-    at = made.data_ptr()
+    # Four allocations take 6 us of host time, one that is split and viewed 12.
+    dev = block_table.device
+    table = _empty((n, width), dtype=_I32, device=dev)
+    lens = _empty(n, dtype=_I32, device=dev)
+    copies = _empty((n, 3), dtype=_I32, device=dev)
+    info = _empty(2, dtype=_I32, device=dev)
+    ws = cache_workspace(n, cache.num_pages, dev) if workspace is None else workspace
+    raw = _raw_stream(table.get_device()) if stream is None else _stream_of(stream, table, lens, copies, info, ws)
     rc = (_L or _lib()).mxfp4_cache_update(
         block_table.data_ptr(), block_table.stride(0) if old > 1 else width, width, seq_lens.data_ptr(), old,
-        parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, at, at + 4 * n * width,
-        at + 4 * n * (width + 1), at + 4 * n * (width + 4), ws.data_ptr(), ws.nbytes, raw)
+        parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, table.data_ptr(),
+        lens.data_ptr(), copies.data_ptr(), info.data_ptr(), ws.data_ptr(), ws.nbytes, raw)
     if rc:
         _fail(rc, "mxfp4_cache_update")
-    return table.view(n, width), lens, copies.view(n, 3), info
+    return table, lens, copies, info
 
 
 def cache_copy(cache, copies, stream=None):
