@@ -306,9 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     // 384 threads start with 168 registers each; the two groups that hold a
     // row of scores per thread take 208, the third keeps 88 (the sum is the same).
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kLoadWarp) {
         Loader<D, SPLIT> ld{p, sh, &kmap, &vmap, wait, base, lane};
         while (next_segment(p, sh.before, unit, unit_end, g)) {
@@ -425,7 +424,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t st = tmem + wg * 128 + lane_at;            // S, then P
