@@ -109,6 +109,24 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Whether any of this thread's share (1 of 128) of a V tile is an infinity or a NaN.
 template <int D>
 __device__ __forceinline__ bool v_not_finite(uint32_t v, int r) {
@@ -198,7 +216,17 @@ struct Loader {
     uint32_t count = 0, patches = 0;
     bool ok = true;
 
-    __device__ void tile(const Segment& g, int step, bool v) {
+    // This lane's box of a tile: its page, or -1. Read well before the copy
+    // that needs it (a table read takes as long as a copy).
+    __device__ int page_for(const Segment& g, int step) const {
+        const CacheView& cv = p.cache;
+        const int box = min(1 << cv.page_shift, kTcKeys), boxes = kTcKeys / box;
+        const int key = (g.it.begin / kTcKeys + g.it.tile + step) * kTcKeys + (lane & (boxes - 1)) * box;
+        if (step >= g.steps || key >= g.it.end || key + box <= g.it.begin) return -1;
+        return page_of(p.batch, g.it.b, key, cv.page_shift, cv.num_pages);
+    }
+
+    __device__ void tile(const Segment& g, int step, bool v, int pg) {
         if (!ok) return;
         const CacheView& cv = p.cache;
         const uint32_t slot = count % L::kSlots, turn = count / L::kSlots;
@@ -219,10 +247,7 @@ struct Loader {
         __syncwarp();
         const uint32_t dst = base + L::kRing + slot * L::kTile;
         if (lane < boxes * (D / 64)) {
-            const int half = lane / boxes, b = lane % boxes, key = key0 + b * box;
-            int pg = -1;
-            if (key < g.it.end && key + box > g.it.begin)
-                pg = page_of(p.batch, g.it.b, key, cv.page_shift, cv.num_pages);
+            const int half = lane / boxes, b = lane & (boxes - 1), key = key0 + b * box;
             // A page coordinate past the pool reads as zeros.
             tma_load_4d(dst + half * L::kHalf + b * box * 128, v ? vmap : kmap, half * 64, key & (page - 1), g.it.head,
                         pg < 0 ? cv.num_pages : pg, bar);
@@ -311,18 +336,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kLoadWarp) {
         Loader<D, SPLIT> ld{p, sh, &kmap, &vmap, wait, base, lane};
         while (next_segment(p, sh.before, unit, unit_end, g)) {
+            int p0 = ld.page_for(g, 0), p1 = ld.page_for(g, 1), p2 = ld.page_for(g, 2);
             if constexpr (SPLIT) {  // the order in which the products need them
-                ld.tile(g, 0, false);
-                if (g.steps > 1) ld.tile(g, 1, false);
-                for (int j = 0; j < g.steps; ++j) {
-                    ld.tile(g, j, true);
-                    if (j + 2 < g.steps) ld.tile(g, j + 2, false);
-                }
-            } else {
-                for (int j = 0; j < g.steps; ++j) {
-                    ld.tile(g, j, false);
-                    ld.tile(g, j, true);
-                }
+                ld.tile(g, 0, false, p0);
+                if (g.steps > 1) ld.tile(g, 1, false, p1);
+            }
+            for (int j = 0; j < g.steps; ++j) {
+                if constexpr (!SPLIT) ld.tile(g, j, false, p0);
+                ld.tile(g, j, true, p0);
+                if (SPLIT && j + 2 < g.steps) ld.tile(g, j + 2, false, p2);
+                p0 = p1;
+                p1 = p2;
+                p2 = ld.page_for(g, j + 3);
             }
         }
         if (!ld.ok && lane == 0) ld.drain();
@@ -499,8 +524,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int c = 0; c < 4; ++c) tmem_load32(st + c * 32, s + c * 32);
                 tc::tmem_wait_ld();
                 if constexpr (CAP) {
+                    // ScoreMap's formula, two scores an instruction where there is one.
+                    const uint64_t mul = f32x2_pack(p.map.mul, p.map.mul), one = f32x2_pack(1.f, 1.f);
+                    const uint64_t cap = f32x2_pack(p.map.cap, p.map.cap), cap2 = f32x2_pack(-2.f * p.map.cap, -2.f * p.map.cap);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = p.map(s[c]);
+                    for (int c = 0; c < 128; c += 2) {
+                        const float2 x = f32x2_unpack(f32x2_mul(f32x2_pack(s[c], s[c + 1]), mul));
+                        const float2 d = f32x2_unpack(f32x2_add(f32x2_pack(exp2_fast(x.x), exp2_fast(x.y)), one));
+                        const float2 t = f32x2_unpack(f32x2_fma(f32x2_pack(rcp_fast(d.x), rcp_fast(d.y)), cap2, cap));
+                        s[c] = t.x;
+                        s[c + 1] = t.y;
+                    }
                 }
                 const int key0 = (it.begin / kTcKeys + it.tile + j) * kTcKeys;
                 // Some row does not see some key of this tile.
@@ -532,8 +566,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 float top4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 4; c < 128; ++c) top4[c & 3] = fmaxf(top4[c & 3], s[c]);
-                float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top4[x] = max3(top4[x], s[c + x], s[c + 4 + x]);
+                float top = max3(max3(top4[0], top4[1], top4[2]), top4[3], max3(s[124], s[125], fmaxf(s[126], s[127])));
                 if constexpr (!CAP) top *= p.map.mul;
                 if (__any_sync(0xffffffffu, top > m + kTcSlack)) {
                     const float up = fmaxf(m, top);
@@ -555,23 +591,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
                 const float base_m = m == -INFINITY ? 0.f : m;
-                float sum0 = 0.f, sum1 = 0.f;
+                uint64_t sum2[2] = {0, 0};
+                const uint64_t mul2 = f32x2_pack(p.map.mul, p.map.mul), one2 = f32x2_pack(1.f, 1.f);
+                const uint64_t neg2 = f32x2_pack(-base_m, -base_m);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        const float a = exp2_fast(CAP ? s[c * 32 + 2 * x] - base_m
-                                                      : fmaf(s[c * 32 + 2 * x], p.map.mul, -base_m));
-                        const float b = exp2_fast(CAP ? s[c * 32 + 2 * x + 1] - base_m
-                                                      : fmaf(s[c * 32 + 2 * x + 1], p.map.mul, -base_m));
-                        sum0 += a;
-                        sum1 += b;
+                        const uint64_t pair = f32x2_pack(s[c * 32 + 2 * x], s[c * 32 + 2 * x + 1]);
+                        const float2 t = f32x2_unpack(f32x2_fma(pair, CAP ? one2 : mul2, neg2));
+                        const float a = exp2_fast(t.x), b = exp2_fast(t.y);
+                        sum2[x & 1] = f32x2_add(sum2[x & 1], f32x2_pack(a, b));
                         w[x] = pack_bf16x2(a, b);
                     }
                     tc::tmem_store16(st + c * 16, w);
                 }
-                l += sum0 + sum1;
+                const float2 sums = f32x2_unpack(f32x2_add(sum2[0], sum2[1]));
+                l += sums.x + sums.y;
                 tc::tmem_wait_st();
                 // V of a key that some rows see and others do not may hold an
                 // infinity or a NaN, and 0 * NaN is NaN: then the rows' own
