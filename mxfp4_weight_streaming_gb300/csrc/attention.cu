@@ -27,6 +27,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 16;                // keys per warp and step
 constexpr int kKeyTile = kKeys * kWarps;  // keys per CTA and step
+constexpr int kKeyShift = 6;
+static_assert(kKeyTile == 1 << kKeyShift);
 constexpr int kRingBytes = 24 * 1024;    // per warp
 constexpr int kCtasPerSm = 2;
 // A running maximum is raised only when a score exceeds it by more than this
@@ -199,10 +201,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
                 const int r = mt * 16 + h * 8 + g;
                 const bool in = r < rows;
                 const int row = it.rt * R + (in ? r : 0);
-                const int i = row / cut.group;
+                const int i = cut.by_group.div(row);
                 tok[mt][h] = in ? i : -1;
                 const __nv_bfloat16* src =
-                    p.q + (it.first + i) * p.q_stride + (it.head * cut.group + row % cut.group) * D;
+                    p.q + (it.first + i) * p.q_stride + (it.head * cut.group + row - i * cut.group) * D;
                 if constexpr (!E4M3) {
                     q_mul[mt][h] = 1.f;
 #pragma unroll
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
             l[mt][0] = l[mt][1] = 0.f;
         }
         // Keys below `open` are visible to every row (without a window).
-        const int open = cut.tree ? start : start + static_cast<int>(static_cast<int64_t>(it.rt) * R / cut.group) + 1;
+        const int open = cut.tree ? start : start + cut.by_group.div(it.rt * R) + 1;
 
 #pragma unroll 1
         for (int step = 0; step < steps; ++step) {
@@ -504,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
                 acc.w += f * x.w;
             }
             if (whole) {
-                const int row = it.rt * R + r, i = row / cut.group;
-                const int64_t to = static_cast<int64_t>(it.first + i) * p.q_heads + it.head * cut.group +
-                                   row % cut.group;
+                const int row = it.rt * R + r, i = cut.by_group.div(row);
+                const int64_t to = static_cast<int64_t>(it.first + i) * p.q_heads + it.head * cut.group + row -
+                                   i * cut.group;
                 const float f = sum == 0.f ? 0.f : vs / sum;
                 uint2 w;
                 w.x = pack_bf16(acc.x * f, acc.y * f);
@@ -530,7 +532,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(Params p, int ctas) {
     constexpr int V = D / 32;  // elements per lane
     const Cut& cut = p.cut;
-    const int R = cut.row_tile;
+    const int R = 1 << cut.row_shift;
     pdl_wait_previous();
     pdl_launch_dependents();
     const Parts parts = parts_in(p.ws, ctas, R, D);
@@ -551,15 +553,16 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(Params p, int 
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < sp.x; ++i) {
-        const float2 ml = parts.ml[slot(i) * R + r];
+    for (int x = 0; x < sp.x; ++x) {
+        const float2 ml = parts.ml[slot(x) * R + r];
         const float f = ml.x == top ? 1.f : exp2_fast(ml.x - base);
         sum += f * ml.y;
-        const float* src = parts.o + (static_cast<int64_t>(slot(i)) * R + r) * D + lane * V;
+        const float* src = parts.o + (static_cast<int64_t>(slot(x)) * R + r) * D + lane * V;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += f * src[j];
     }
-    const int64_t to = static_cast<int64_t>(first + row / cut.group) * p.q_heads + sp.w * cut.group + row % cut.group;
+    const int i = cut.by_group.div(row);
+    const int64_t to = static_cast<int64_t>(first + i) * p.q_heads + sp.w * cut.group + row - i * cut.group;
     const float vs = E4M3 && p.cache.v_scale ? p.cache.v_scale[sp.w] : 1.f;
     const float f = sum == 0.f ? 0.f : vs / sum;
 #pragma unroll
@@ -598,7 +601,7 @@ bool use_tc(int64_t rows, bool e4m3) { return !e4m3 && rows > 32; }
 }  // namespace
 
 cudaError_t launch_join(const Params& p, bool e4m3, int ctas, cudaStream_t stream) {
-    PdlLaunch j(dim3(ctas, p.cut.row_tile / kWarps), dim3(kThreads), 0, stream);
+    PdlLaunch j(dim3(ctas, (1 << p.cut.row_shift) / kWarps), dim3(kThreads), 0, stream);
     if (p.cache.head_dim == 64)
         return e4m3 ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, true>, p, ctas)
                     : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, false>, p, ctas);
@@ -626,6 +629,7 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
     p.status = a.status;
     p.q_heads = a.q_heads;
     p.cut.group = a.q_heads / cache.kv_heads;
+    p.cut.by_group = attn::divisor(p.cut.group);
     p.cut.kv_heads = cache.kv_heads;
     p.cut.window = a.window;
     p.cut.tree = a.tree_mask != nullptr;
@@ -641,8 +645,8 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
     }
     p.map = attn::score_map(a.scale, a.softcap);
     const int mt = rows <= 16 ? 1 : 2;
-    p.cut.row_tile = 16 * mt;
-    p.cut.key_tile = attn::kKeyTile;
+    p.cut.row_shift = mt == 1 ? 4 : 5;
+    p.cut.key_shift = attn::kKeyShift;
     const int ctas = attn::kCtasPerSm * num_sms;
     return cache.head_dim == 64 ? attn::launch_d<64>(p, a.e4m3, mt, ctas, stream)
                                 : attn::launch_d<128>(p, a.e4m3, mt, ctas, stream);

@@ -22,12 +22,35 @@ namespace attn {
 constexpr int kGroups = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Cut of one call.
+// n / d for n < 2^31 by a multiplication: with s = ceil(log2 d) and m =
+// ceil(2^(31 + s) / d), m d - 2^(31 + s) < d <= 2^s keeps the quotient exact.
+struct Divisor {
+    uint32_t d, m, s;
+    __host__ __device__ __forceinline__ int div(int n) const {
+#ifdef __CUDA_ARCH__
+        return s == 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m) >> (s - 1));
+#else
+        return static_cast<int>(static_cast<uint32_t>(n) / d);
+#endif
+    }
+};
+
+inline Divisor divisor(int d) {
+    Divisor v{};
+    v.d = static_cast<uint32_t>(d);
+    while ((1u << v.s) < v.d) ++v.s;
+    v.m = v.s == 0 ? 0 : static_cast<uint32_t>(((uint64_t(1) << (31 + v.s)) + v.d - 1) / v.d);
+    return v;
+}
+
+// Cut of one call. Rows of a request, n * group, stay below 2^31 (2^24 tokens
+// and 128 heads a group at most).
 struct Cut {
     int group;       // query heads per KV head
+    Divisor by_group;
     int kv_heads;
-    int row_tile;    // R
-    int key_tile;    // keys per unit of work
+    int row_shift;   // R = 1 << row_shift
+    int key_shift;   // keys per unit of work
     int window;      // 0: none
     bool tree;
     int min_share;   // units a CTA takes at least
@@ -36,8 +59,8 @@ struct Cut {
 // Keys [begin, end) that some row of row tile rt of a request sees; begin is
 // rounded down to a key tile only where tiles are counted.
 __device__ __forceinline__ void item_keys(const Cut& c, int n, int seq, int rt, int& begin, int& end) {
-    const int tok0 = static_cast<int>(static_cast<int64_t>(rt) * c.row_tile / c.group);
-    const int tok1 = min(n - 1, static_cast<int>((static_cast<int64_t>(rt) * c.row_tile + c.row_tile - 1) / c.group));
+    const int tok0 = c.by_group.div(rt << c.row_shift);
+    const int tok1 = min(n - 1, c.by_group.div((rt << c.row_shift) + (1 << c.row_shift) - 1));
     end = c.tree ? seq : max(seq - n + tok1 + 1, 0);
     begin = c.window ? max(seq - n + tok0 - c.window + 1, 0) : 0;
     end = max(end, begin);
@@ -46,11 +69,11 @@ __device__ __forceinline__ void item_keys(const Cut& c, int n, int seq, int rt, 
 __device__ __forceinline__ int item_tiles(const Cut& c, int n, int seq, int rt) {
     int begin, end;
     item_keys(c, n, seq, rt, begin, end);
-    return max((end + c.key_tile - 1) / c.key_tile - begin / c.key_tile, 1);
+    return max(((end + (1 << c.key_shift) - 1) >> c.key_shift) - (begin >> c.key_shift), 1);
 }
 
 __device__ __forceinline__ int row_tiles(const Cut& c, int n) {
-    return static_cast<int>((static_cast<int64_t>(n) * c.group + c.row_tile - 1) / c.row_tile);
+    return (n * c.group + (1 << c.row_shift) - 1) >> c.row_shift;
 }
 
 __device__ __forceinline__ int64_t request_units(const Cut& c, const BatchView& bt, int page_shift, int b) {
@@ -123,8 +146,9 @@ __device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int pa
         rem -= block;
         ++it.rt;
     }
-    it.head = static_cast<int>(rem / it.tiles);
-    it.tile = static_cast<int>(rem % it.tiles);
+    const uint32_t tiles = it.tiles;
+    it.head = static_cast<int>(rem >> 32 ? rem / tiles : static_cast<uint32_t>(rem) / tiles);
+    it.tile = static_cast<int>(rem - it.head * static_cast<int64_t>(tiles));
     item_keys(c, it.n, it.seq, it.rt, it.begin, it.end);
     return it;
 }

@@ -51,7 +51,7 @@ struct Layout {
 template <bool SPLIT>
 struct Shared {
     int64_t before[kGroups + 1];
-    uint64_t kv_full[8], kv_empty[8], patch, q_full[2], s_full[2], p_full[2], pv_done[2], vote[2], meet, drain;
+    uint64_t kv_full[8], kv_empty[8], patch, q_full[2], s_full[2], p_full[2][2], pv_done[2], vote[2], meet, drain;
     float m[2][SPLIT ? 128 : 1], l[2][SPLIT ? 128 : 1];  // of the two streams' rows
     uint32_t tmem;
     uint32_t bad[2];   // last tile (counted from 1) of each stream whose V is not finite
@@ -127,6 +127,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
 // Whether any of this thread's share (1 of 128) of a V tile is an infinity or a NaN.
 template <int D>
 __device__ __forceinline__ bool v_not_finite(uint32_t v, int r) {
@@ -196,7 +202,7 @@ __device__ __forceinline__ bool next_segment(const Params& p, const int64_t* bef
     if (unit >= unit_end) return false;
     g.it = locate(p.cut, p.batch, p.cache.page_shift, before, unit);
     g.steps = static_cast<int>(min(unit_end - unit, static_cast<int64_t>(g.it.tiles - g.it.tile)));
-    g.rows = min(p.cut.row_tile, g.it.n * p.cut.group - g.it.rt * p.cut.row_tile);
+    g.rows = min(1 << p.cut.row_shift, g.it.n * p.cut.group - (g.it.rt << p.cut.row_shift));
     g.whole = g.it.tile == 0 && g.steps == g.it.tiles;
     g.unit = unit;
     unit += g.steps;
@@ -292,7 +298,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cut& cut = p.cut;
-    const Parts parts = parts_in(p.ws, gridDim.x, cut.row_tile, D);
+    constexpr int R = SPLIT ? 128 : 256;  // rows of a row tile
+    const Parts parts = parts_in(p.ws, gridDim.x, R, D);
     const WaitCtx wait{p.status, &sh.abort};
 
     if (warp == kMmaWarp) {
@@ -309,7 +316,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&sh.q_full[s]), SPLIT ? 256 : 128);
             mbar_init(smem_addr(&sh.s_full[s]), 1);
-            mbar_init(smem_addr(&sh.p_full[s]), 128);
+            mbar_init(smem_addr(&sh.p_full[s][0]), 128);
+            mbar_init(smem_addr(&sh.p_full[s][1]), 128);
             mbar_init(smem_addr(&sh.pv_done[s]), 1);
             mbar_init(smem_addr(&sh.vote[s]), 128);
             sh.bad[s] = sh.skip[s] = 0;
@@ -352,100 +360,96 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!ld.ok && lane == 0) ld.drain();
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            const uint32_t idesc_qk = idesc_f16(kTcKeys, false), idesc_pv = idesc_f16(D, true);
-            uint32_t used = 0;         // ring tiles taken
-            uint32_t q_turn = 0;       // items begun
-            uint32_t done[2] = {0, 0}; // probabilities taken, per stream
-            bool ok = true;
-            auto tile_ready = [&](uint32_t n) {
-                ok = ok && mbar_wait(smem_addr(&sh.kv_full[n % L::kSlots]), (n / L::kSlots) & 1, wait);
-                tc::fence_after_sync();
-                return ok;
-            };
-            auto qk = [&](int s, uint32_t n) {
-                const uint32_t q = base + (SPLIT ? 0 : s * L::kTile), k = base + L::kRing + (n % L::kSlots) * L::kTile;
+        // All lanes walk through the tiles, so that what the products are
+        // given stays in uniform registers; one lane issues.
+        const uint32_t idesc_qk = idesc_f16(kTcKeys, false), idesc_pv = idesc_f16(D, true);
+        const uint64_t q_desc = tc::operand_desc(base), k_desc = tc::operand_desc(base + L::kRing);
+        const uint64_t v_desc = tc::smem_desc(base + L::kRing, L::kHalf, 1024, tc::kLayoutSwizzle128);
+        const bool one = elect_one();
+        uint32_t used = 0;         // ring tiles taken
+        uint32_t q_turn = 0;       // items begun
+        uint32_t done[2] = {0, 0}; // probabilities taken, per stream
+        bool ok = true;
+        auto wait_for = [&](uint64_t& bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_addr(&bar), parity, wait));
+            return ok;
+        };
+        auto tile_ready = [&](uint32_t n) { return wait_for(sh.kv_full[n % L::kSlots], (n / L::kSlots) & 1); };
+        auto qk = [&](int s, uint32_t n, bool frees) {
+            const uint64_t q = q_desc + (SPLIT ? 0 : (s * L::kTile) >> 4);
+            const uint64_t k = k_desc + (n % L::kSlots) * (L::kTile >> 4);
+            tc::fence_after_sync();
+            if (one) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = (i >> 2) * L::kHalf + (i & 3) * 32;
-                    mma_ss(tmem + s * 128, tc::operand_desc(q + off), tc::operand_desc(k + off), idesc_qk, i > 0);
+                    const uint32_t off = ((i >> 2) * L::kHalf + (i & 3) * 32) >> 4;
+                    mma_ss(tmem + s * 128, q + off, k + off, idesc_qk, i > 0);
                 }
                 tc::commit_to(smem_addr(&sh.s_full[s]));
-            };
-            auto pv = [&](int s, uint32_t n, bool first) {
-                const uint32_t v = base + L::kRing + (n % L::kSlots) * L::kTile;
-                if (!lds_u32_volatile(smem_addr(&sh.skip[s])))
-#pragma unroll
-                    for (int i = 0; i < kTcKeys / 16; ++i)
-                        mma_ts(tmem + 256 + s * D, tmem + s * 128 + i * 8,
-                               tc::smem_desc(v + i * 2048, L::kHalf, 1024, tc::kLayoutSwizzle128), idesc_pv,
-                               !(first && i == 0));
-                tc::commit_to(smem_addr(&sh.pv_done[s]));
-            };
-            auto free_tile = [&](uint32_t n) { tc::commit_to(smem_addr(&sh.kv_empty[n % L::kSlots])); };
-            auto probs_ready = [&](int s) {
-                ok = ok && mbar_wait(smem_addr(&sh.p_full[s]), done[s] & 1, wait);
-                ++done[s];
-                tc::fence_after_sync();
-                return ok;
-            };
-            auto q_ready = [&](int s) {
-                ok = ok && mbar_wait(smem_addr(&sh.q_full[s]), q_turn & 1, wait);
-                tc::fence_after_sync();
-                return ok;
-            };
-            while (ok && next_segment(p, sh.before, unit, unit_end, g)) {
-                if constexpr (SPLIT) {
-                    if (!q_ready(0)) break;
-                    // Ring order: K0 K1 V0 K2 V1 K3 ...
-                    const uint32_t u0 = used;
-                    const int n = g.steps;
-                    auto k_at = [&](int j) { return u0 + (j < 2 ? j : 2 * j - 1); };
-                    auto v_at = [&](int j) { return u0 + min(n, j + 2) + j; };
-                    for (int j = 0; j < min(n, 2) && ok; ++j) {
-                        if (!tile_ready(k_at(j))) break;
-                        qk(j & 1, k_at(j));
-                        free_tile(k_at(j));
-                    }
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int s = j & 1;
-                        if (!probs_ready(s) || !tile_ready(v_at(j))) break;
-                        pv(s, v_at(j), j < 2);
-                        free_tile(v_at(j));
-                        if (j + 2 < n) {
-                            if (!tile_ready(k_at(j + 2))) break;
-                            qk(s, k_at(j + 2));
-                            free_tile(k_at(j + 2));
-                        }
-                    }
-                } else {
-                    for (int s = 0; s < 2 && ok; ++s) {
-                        if (!q_ready(s) || !tile_ready(used)) break;
-                        qk(s, used);
-                    }
-                    if (ok) free_tile(used);
-                    for (int j = 0; j < g.steps && ok; ++j) {
-                        const uint32_t v = used + 2 * j + 1, k = v + 1;
-                        for (int s = 0; s < 2; ++s) {
-                            if (!probs_ready(s) || !tile_ready(v)) break;
-                            pv(s, v, j == 0);
-                            if (s == 1) free_tile(v);
-                            if (j + 1 < g.steps) {
-                                if (!tile_ready(k)) break;
-                                qk(s, k);
-                                if (s == 1) free_tile(k);
-                            }
-                        }
-                    }
-                }
-                used += 2 * g.steps;
-                ++q_turn;
+                if (frees) tc::commit_to(smem_addr(&sh.kv_empty[n % L::kSlots]));
             }
-            if (!ok) {  // products in flight end before TMEM is given back
-                tc::commit_to(smem_addr(&sh.drain));
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(smem_addr(&sh.drain), 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            __syncwarp();
+        };
+        // The two halves of a tile's keys: the second half's probabilities
+        // come while the first half's product runs.
+        auto pv = [&](int s, uint32_t n, bool first, bool frees) {
+            const uint64_t v = v_desc + (n % L::kSlots) * (L::kTile >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!wait_for(sh.p_full[s][h], done[s] & 1)) return false;
+                tc::fence_after_sync();
+                const bool skip = lds_u32_volatile(smem_addr(&sh.skip[s])) != 0;
+                if (one && !skip) {
+#pragma unroll
+                    for (int i = h * kTcKeys / 32; i < (h + 1) * kTcKeys / 32; ++i)
+                        mma_ts(tmem + 256 + s * D, tmem + s * 128 + i * 8, v + i * (2048 >> 4), idesc_pv,
+                               !(first && i == 0));
                 }
+            }
+            if (one) {
+                tc::commit_to(smem_addr(&sh.pv_done[s]));
+                if (frees) tc::commit_to(smem_addr(&sh.kv_empty[n % L::kSlots]));
+            }
+            __syncwarp();
+            ++done[s];
+            return true;
+        };
+        while (ok && next_segment(p, sh.before, unit, unit_end, g)) {
+            const int n = __shfl_sync(0xffffffffu, g.steps, 0);
+            if constexpr (SPLIT) {
+                if (!wait_for(sh.q_full[0], q_turn & 1)) break;
+                // Ring order: K0 K1 V0 K2 V1 K3 ...
+                auto k_at = [&](int j) { return used + (j < 2 ? j : 2 * j - 1); };
+                auto v_at = [&](int j) { return used + min(n, j + 2) + j; };
+                for (int j = 0; j < min(n, 2) && tile_ready(k_at(j)); ++j) qk(j, k_at(j), true);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = j & 1;
+                    if (!tile_ready(v_at(j)) || !pv(s, v_at(j), j < 2, true)) break;
+                    if (j + 2 < n && tile_ready(k_at(j + 2))) qk(s, k_at(j + 2), true);
+                }
+            } else {
+                if (!tile_ready(used)) break;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (wait_for(sh.q_full[s], q_turn & 1)) qk(s, used, s == 1);
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t v = used + 2 * j + 1, k = v + 1;
+                    const bool more = j + 1 < n;
+                    if (!tile_ready(v)) break;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (!pv(s, v, j == 0, s == 1)) break;
+                        if (more && (s == 1 || tile_ready(k))) qk(s, k, s == 1);
+                    }
+                }
+            }
+            used += 2 * n;
+            ++q_turn;
+        }
+        if (!ok && one) {  // products in flight end before TMEM is given back
+            tc::commit_to(smem_addr(&sh.drain));
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(smem_addr(&sh.drain), 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
         __syncwarp();
@@ -473,11 +477,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // q rows of a segment into shared memory: this stream's 128 rows, or
         // (SPLIT) half of the elements of the one 128-row tile.
         auto load_q = [&](const Segment& s) {
-            const int row = s.it.rt * cut.row_tile + (SPLIT ? 0 : wg * 128) + r;
+            const int row = s.it.rt * R + (SPLIT ? 0 : wg * 128) + r;
             const bool in = (SPLIT ? 0 : wg * 128) + r < s.rows;
-            const int i = in ? row / cut.group : 0;
+            const int i = in ? cut.by_group.div(row) : 0;
             const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + (s.it.first + i) * p.q_stride + (s.it.head * cut.group + (in ? row % cut.group : 0)) * D);
+                p.q + (s.it.first + i) * p.q_stride + (s.it.head * cut.group + (in ? row - i * cut.group : 0)) * D);
             const uint32_t dst = base + (SPLIT ? 0 : wg * L::kTile);
             constexpr int N = SPLIT ? D / 16 : D / 8;
             const int c0 = SPLIT ? wg * N : 0;
@@ -498,16 +502,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (more) load_q(g);
         while (more && ok) {
             const Item& it = g.it;
-            const int row = it.rt * cut.row_tile + (SPLIT ? 0 : wg * 128) + r;
+            const int row = it.rt * R + (SPLIT ? 0 : wg * 128) + r;
             const bool in = (SPLIT ? 0 : wg * 128) + r < g.rows;
-            const int tok = in ? row / cut.group : 0;
+            const int tok = in ? cut.by_group.div(row) : 0;
             const int start = it.seq - it.n, pos = start + tok;
             // Keys below `open` are visible to every row of the tile (without a window).
-            const int open =
-                cut.tree ? start : start + static_cast<int>(static_cast<int64_t>(it.rt) * cut.row_tile / cut.group) + 1;
+            const int open = cut.tree ? start : start + cut.by_group.div(it.rt * R) + 1;
             // Keys from `all_from` on have left no row's window.
-            const int all_from = start + min(it.n - 1, static_cast<int>((static_cast<int64_t>(it.rt + 1) * cut.row_tile - 1) / cut.group)) -
-                                 cut.window + 1;
+            const int all_from = start + min(it.n - 1, cut.by_group.div((it.rt + 1) * R - 1)) - cut.window + 1;
             // This row's first and last visible key.
             const int first = max(it.begin, cut.window ? pos - cut.window + 1 : 0);
             const int last = in ? min(cut.tree ? it.seq - 1 : pos, it.end - 1) : -1;
@@ -590,6 +592,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
+                if (skipped && !edge) {  // before this tile's first half is handed over
+                    if (r == 0) sts_u32_volatile(smem_addr(&sh.skip[wg]), 0);
+                    skipped = false;
+                }
                 const float base_m = m == -INFINITY ? 0.f : m;
                 uint64_t sum2[2] = {0, 0};
                 const uint64_t mul2 = f32x2_pack(p.map.mul, p.map.mul), one2 = f32x2_pack(1.f, 1.f);
@@ -606,6 +612,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         w[x] = pack_bf16x2(a, b);
                     }
                     tc::tmem_store16(st + c * 16, w);
+                    if (c == 1 && !edge) {
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        mbar_arrive(smem_addr(&sh.p_full[wg][0]));
+                    }
                 }
                 const float2 sums = f32x2_unpack(f32x2_add(sum2[0], sum2[1]));
                 l += sums.x + sums.y;
@@ -628,11 +639,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::fence_after_sync();
                         add_tile_by_rows<D>(ot, st, v, L::kHalf, jj == 0);
                     }
+                    if (r == 0) sts_u32_volatile(smem_addr(&sh.skip[wg]), bad);
+                    skipped = bad;
                 }
-                if (r == 0 && bad != skipped) sts_u32_volatile(smem_addr(&sh.skip[wg]), bad);
-                skipped = bad;
                 tc::fence_before_sync();
-                mbar_arrive(smem_addr(&sh.p_full[wg]));
+                if (edge) mbar_arrive(smem_addr(&sh.p_full[wg][0]));
+                mbar_arrive(smem_addr(&sh.p_full[wg][1]));
             }
             if constexpr (SPLIT) {
                 sh.m[wg][r] = m;
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (ok) {
                 const int64_t to = static_cast<int64_t>(cur.it.first + tok) * p.q_heads + cur.it.head * cut.group +
-                                   (in ? row % cut.group : 0);
+                                   (in ? row - tok * cut.group : 0);
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 // SPLIT: each group takes half of the columns of both accumulators.
                 constexpr int CH = SPLIT ? D / 64 : D / 32;
@@ -706,14 +718,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                 pack_bf16x2(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
                     } else {
                         float4* dst = reinterpret_cast<float4*>(
-                            parts.o + (static_cast<int64_t>(slot) * cut.row_tile + tr) * D + col);
+                            parts.o + (static_cast<int64_t>(slot) * R + tr) * D + col);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
                             dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                     }
                 }
                 if (in && (!SPLIT || wg == 0)) {
-                    if (!cur.whole) parts.ml[slot * cut.row_tile + tr] = make_float2(topm, sum);
+                    if (!cur.whole) parts.ml[slot * R + tr] = make_float2(topm, sum);
                     else if (p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (topm + log2f(sum)) / kLog2e;
                 }
             }
@@ -801,12 +813,12 @@ size_t tc_workspace_bytes(int64_t rows, int d, int num_sms) { return parts_bytes
 
 cudaError_t launch_tc(const Params& in, int64_t rows, int num_sms, cudaStream_t stream) {
     Params p = in;
-    p.cut.row_tile = row_tile_of(rows);
-    p.cut.key_tile = kTcKeys;
+    p.cut.row_shift = row_tile_of(rows) == 128 ? 7 : 8;
+    p.cut.key_shift = 7;
     const MapSlot* maps = nullptr;
     cudaError_t e = pool_maps(p.cache, &maps);
     if (e != cudaSuccess) return e;
-    const bool split = p.cut.row_tile == 128;
+    const bool split = p.cut.row_shift == 7;
     e = p.cache.head_dim == 64 ? launch_d<64>(p, split, maps->kmap, maps->vmap, num_sms, stream)
                                : launch_d<128>(p, split, maps->kmap, maps->vmap, num_sms, stream);
     return e == cudaSuccess ? launch_join(p, false, num_sms, stream) : e;
