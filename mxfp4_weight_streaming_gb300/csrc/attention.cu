@@ -142,14 +142,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     const Parts parts = parts_in(p.ws, gridDim.x, R, D);
 
     pdl_wait_previous();
-    const int64_t total = count_units(cut, p.batch, cv.page_shift, s_before);
+    const int64_t total = count_units<kThreads>(cut, p.batch, threadIdx.x, s_before);
     const int64_t share = share_of(cut, total, gridDim.x);
     int64_t unit = share * blockIdx.x;
     const int64_t unit_end = min(unit + share, total);
     if (threadIdx.x == 0) parts.split[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     while (unit < unit_end) {
-        const Item it = locate(cut, p.batch, cv.page_shift, s_before, unit);
+        const Item it = locate(cut, p.batch, s_before, unit);
         const int steps = static_cast<int>(min(unit_end - unit, static_cast<int64_t>(it.tiles - it.tile)));
         const int rows = min(R, it.n * cut.group - it.rt * R);
         const int start = it.seq - it.n;  // cache index of the first new token
@@ -526,49 +526,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     pdl_launch_dependents();
 }
 
-// Joins the parts of items that several CTAs shared: block (c, y) takes rows
-// of the item that begins in CTA c, one warp per row.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(Params p, int ctas) {
-    constexpr int V = D / 32;  // elements per lane
+// Joins the parts of items that several CTAs shared: block (c, y) takes 32
+// rows of the item that begins in CTA c, and a thread 4 elements of a row.
+// Neighbouring threads are neighbours in the order of the parts: elements of
+// a row, or (parts of attention_tc.cu) rows.
+constexpr int kJoinThreads = 256;
+template <int D, bool E4M3, bool FROM_TC>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(Params p, int ctas) {
     const Cut& cut = p.cut;
-    const int R = 1 << cut.row_shift;
+    const int R = 1 << cut.row_shift, rows_here = min(R, 32);
     pdl_wait_previous();
     pdl_launch_dependents();
     const Parts parts = parts_in(p.ws, ctas, R, D);
     const int4 sp = parts.split[blockIdx.x];
     if (sp.x == 0) return;
     int first, n, seq;
-    request_extent(p.batch, sp.y, p.cache.page_shift, first, n, seq);
-    const int r = blockIdx.y * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int row = sp.z * R + r;
-    if (r >= R || row >= n * cut.group) return;
-    auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
-    float top = -INFINITY;
-    for (int i = lane; i < sp.x; i += 32) top = fmaxf(top, parts.ml[slot(i) * R + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
-    float acc[V], sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < sp.x; ++x) {
-        const float2 ml = parts.ml[slot(x) * R + r];
-        const float f = ml.x == top ? 1.f : exp2_fast(ml.x - base);
-        sum += f * ml.y;
-        const float* src = parts.o + (static_cast<int64_t>(slot(x)) * R + r) * D + lane * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += f * src[j];
-    }
-    const int i = cut.by_group.div(row);
-    const int64_t to = static_cast<int64_t>(first + i) * p.q_heads + sp.w * cut.group + row - i * cut.group;
+    request_extent(p.batch, sp.y, first, n, seq);
     const float vs = E4M3 && p.cache.v_scale ? p.cache.v_scale[sp.w] : 1.f;
-    const float f = sum == 0.f ? 0.f : vs / sum;
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-        *reinterpret_cast<uint32_t*>(p.out + to * D + lane * V + j) = pack_bf16(acc[j] * f, acc[j + 1] * f);
-    if (p.lse && lane == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
+    for (int v = threadIdx.x; v < rows_here * (D / 4); v += kJoinThreads) {
+        const int r = blockIdx.y * 32 + (FROM_TC ? v % 32 : v / (D / 4)), d4 = FROM_TC ? v / 32 : v % (D / 4);
+        const int row = sp.z * R + r, tok = cut.by_group.div(row), head = row - tok * cut.group;
+        if (tok >= n) continue;
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int x = 0; x < sp.x; ++x) top = fmaxf(top, parts.ml[slot(x) * R + r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int x = 0; x < sp.x; ++x) {
+            const float2 ml = parts.ml[slot(x) * R + r];
+            const float f = ml.x == top ? 1.f : exp2_fast(ml.x - base);
+            const int64_t at = static_cast<int64_t>(slot(x)) * R * (D / 4) + (FROM_TC ? d4 * R + r : r * (D / 4) + d4);
+            const float4 o = reinterpret_cast<const float4*>(parts.o)[at];
+            sum += f * ml.y;
+            acc.x += f * o.x;
+            acc.y += f * o.y;
+            acc.z += f * o.z;
+            acc.w += f * o.w;
+        }
+        const int64_t to = static_cast<int64_t>(first + tok) * p.q_heads + sp.w * cut.group + head;
+        const float f = sum == 0.f ? 0.f : vs / sum;
+        *reinterpret_cast<uint2*>(p.out + to * D + 4 * d4) =
+            make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+        if (p.lse && d4 == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    }
 }
 
 template <int D, bool E4M3, int MT>
@@ -585,7 +588,7 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
     }
     PdlLaunch l(dim3(ctas), dim3(kThreads), smem, stream);
     e = cudaLaunchKernelEx(&l.cfg, attention_rows_kernel<D, E4M3, MT>, p);
-    return e == cudaSuccess ? launch_join(p, E4M3, ctas, stream) : e;
+    return e == cudaSuccess ? launch_join(p, E4M3, false, ctas, stream) : e;
 }
 
 template <int D>
@@ -596,17 +599,22 @@ cudaError_t launch_d(const Params& p, bool e4m3, int mt, int ctas, cudaStream_t 
 
 // The tensor-core kernel where the rows of a KV head fill enough of its
 // 128-row tiles.
-bool use_tc(int64_t rows, bool e4m3) { return !e4m3 && rows > 32; }
+bool use_tc(int64_t rows, bool e4m3) { return rows > (e4m3 ? 32 : 16); }
+
+template <int D, bool E4M3>
+cudaError_t launch_join_d(const PdlLaunch& j, const Params& p, bool from_tc, int ctas) {
+    return from_tc ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<D, E4M3, true>, p, ctas)
+                   : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<D, E4M3, false>, p, ctas);
+}
 
 }  // namespace
 
-cudaError_t launch_join(const Params& p, bool e4m3, int ctas, cudaStream_t stream) {
-    PdlLaunch j(dim3(ctas, (1 << p.cut.row_shift) / kWarps), dim3(kThreads), 0, stream);
+cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cudaStream_t stream) {
+    const int blocks = ((1 << p.cut.row_shift) + 31) / 32;
+    PdlLaunch j(dim3(ctas, blocks), dim3(kJoinThreads), 0, stream);
     if (p.cache.head_dim == 64)
-        return e4m3 ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, true>, p, ctas)
-                    : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<64, false>, p, ctas);
-    return e4m3 ? cudaLaunchKernelEx(&j.cfg, attention_join_kernel<128, true>, p, ctas)
-                : cudaLaunchKernelEx(&j.cfg, attention_join_kernel<128, false>, p, ctas);
+        return e4m3 ? launch_join_d<64, true>(j, p, from_tc, ctas) : launch_join_d<64, false>(j, p, from_tc, ctas);
+    return e4m3 ? launch_join_d<128, true>(j, p, from_tc, ctas) : launch_join_d<128, false>(j, p, from_tc, ctas);
 }
 
 }  // namespace attn
@@ -638,10 +646,10 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
     p.batch = batch;
     const int64_t rows = static_cast<int64_t>(a.max_q) * p.cut.group;
     if (attn::use_tc(rows, a.e4m3)) {
-        p.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
+        p.negate = a.scale < 0.f;
         // Masked scores are -inf and are multiplied by `mul`: it may not be 0.
         p.map = attn::score_map(fmaxf(fabsf(a.scale), 1e-36f), a.softcap);
-        return attn::launch_tc(p, rows, num_sms, stream);
+        return attn::launch_tc(p, a.e4m3, rows, num_sms, stream);
     }
     p.map = attn::score_map(a.scale, a.softcap);
     const int mt = rows <= 16 ? 1 : 2;

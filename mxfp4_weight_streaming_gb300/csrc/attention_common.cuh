@@ -19,7 +19,7 @@ namespace attn {
 
 // Requests are counted in at most this many groups of neighbours (one request
 // each up to that many), so the sums fit beside full-size tiles.
-constexpr int kGroups = 128;
+constexpr int kGroups = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // n / d for n < 2^31 by a multiplication: with s = ceil(log2 d) and m =
@@ -76,9 +76,9 @@ __device__ __forceinline__ int row_tiles(const Cut& c, int n) {
     return (n * c.group + (1 << c.row_shift) - 1) >> c.row_shift;
 }
 
-__device__ __forceinline__ int64_t request_units(const Cut& c, const BatchView& bt, int page_shift, int b) {
+__device__ __forceinline__ int64_t request_units(const Cut& c, const BatchView& bt, int b) {
     int first, n, seq;
-    request_extent(bt, b, page_shift, first, n, seq);
+    request_extent(bt, b, first, n, seq);
     int64_t u = 0;
     for (int rt = row_tiles(c, n) - 1; rt >= 0; --rt) u += item_tiles(c, n, seq, rt);
     return u * c.kv_heads;
@@ -86,33 +86,39 @@ __device__ __forceinline__ int64_t request_units(const Cut& c, const BatchView& 
 
 __device__ __forceinline__ int requests_per_group(const BatchView& bt) { return (bt.batch + kGroups - 1) / kGroups; }
 
-// Units of work before each group of requests, and in all (before[groups]);
-// all threads of the block call it.
-__device__ __forceinline__ int64_t count_units(const Cut& c, const BatchView& bt, int page_shift, int64_t* before) {
+// Units of work before each group of requests; returns their sum. Called by
+// THREADS threads (a warp, or the whole block), t = 0 .. THREADS - 1.
+template <int THREADS>
+__device__ __forceinline__ int64_t count_units(const Cut& c, const BatchView& bt, int t, int64_t* before) {
     const int per = requests_per_group(bt), groups = (bt.batch + per - 1) / per;
-    for (int i = threadIdx.x; i < groups; i += blockDim.x) {
+    auto sync = [] {
+        if constexpr (THREADS == 32) __syncwarp();
+        else __syncthreads();
+    };
+#pragma unroll 2
+    for (int i = t; i < groups; i += THREADS) {
         int64_t u = 0;
-        for (int b = i * per; b < min((i + 1) * per, bt.batch); ++b) u += request_units(c, bt, page_shift, b);
+        for (int b = i * per; b < min((i + 1) * per, bt.batch); ++b) u += request_units(c, bt, b);
         before[i + 1] = u;
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
+    sync();
+    if (t < 32) {
         int64_t carry = 0;
         for (int i0 = 0; i0 < groups; i0 += 32) {
-            const int i = i0 + threadIdx.x;
+            const int i = i0 + t;
             int64_t v = i < groups ? before[i + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
-                if (static_cast<int>(threadIdx.x) >= o) v += t;
+                const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+                if (t >= o) v += x;
             }
             v += carry;
             if (i < groups) before[i + 1] = v;
             carry = __shfl_sync(0xffffffffu, v, 31);
         }
-        if (threadIdx.x == 0) before[0] = 0;
+        if (t == 0) before[0] = 0;
     }
-    __syncthreads();
+    sync();
     return before[groups];
 }
 
@@ -123,7 +129,7 @@ struct Item {
     int tile, tiles;        // the unit's key tile within the item, and the item's count
 };
 
-__device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int page_shift, const int64_t* before,
+__device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, const int64_t* before,
                                        int64_t unit) {
     Item it;
     const int per = requests_per_group(bt);
@@ -136,8 +142,8 @@ __device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int pa
     int64_t rem = unit - before[lo];
     it.b = lo * per;
     if (per > 1)
-        for (int64_t u; rem >= (u = request_units(c, bt, page_shift, it.b)); ++it.b) rem -= u;
-    request_extent(bt, it.b, page_shift, it.first, it.n, it.seq);
+        for (int64_t u; rem >= (u = request_units(c, bt, it.b)); ++it.b) rem -= u;
+    request_extent(bt, it.b, it.first, it.n, it.seq);
     it.rt = 0;
     while (true) {
         it.tiles = item_tiles(c, it.n, it.seq, it.rt);
@@ -154,13 +160,17 @@ __device__ __forceinline__ Item locate(const Cut& c, const BatchView& bt, int pa
 }
 
 __device__ __forceinline__ int64_t share_of(const Cut& c, int64_t total, int ctas) {
-    return max((total + ctas - 1) / ctas, static_cast<int64_t>(c.min_share));
+    // 64-bit divisions are long: taken only where they are needed.
+    const int64_t share = total >> 31 ? (total + ctas - 1) / ctas
+                                      : (static_cast<uint32_t>(total) + static_cast<uint32_t>(ctas) - 1u) /
+                                            static_cast<uint32_t>(ctas);
+    return max(share, static_cast<int64_t>(c.min_share));
 }
 
 // Partial results: two slots per CTA, slot 2c for a part that began before
 // the CTA's run and 2c + 1 for one that begins in it.
 struct Parts {
-    float* o;        // [2 ctas][R][D], not divided by the sum
+    float* o;        // [2 ctas], not divided by the sum: [R][D], or from attention_tc.cu [D / 4][R][4]
     float2* ml;      // [2 ctas][R]: running maximum (of log2 scores) and sum
     int4* split;     // [ctas]: parts of the item that begins in CTA c and ends beyond it (0: none), request, row tile, KV head
 };
@@ -207,7 +217,7 @@ struct Params {
     void* ws;
     unsigned* status;
     int q_heads;
-    uint32_t q_flip;  // attention_tc.cu: sign bits to flip in q (a negative scale)
+    bool negate;  // attention_tc.cu: the scale is negative (map has its magnitude)
     ScoreMap map;
     Cut cut;
     CacheView cache;
@@ -215,11 +225,11 @@ struct Params {
 };
 
 // Joins the parts that `ctas` CTAs left in the workspace (attention.cu).
-cudaError_t launch_join(const Params& p, bool e4m3, int ctas, cudaStream_t stream);
+cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cudaStream_t stream);
 
-// The tensor-core kernel (attention_tc.cu): bf16 caches, any number of rows.
+// The tensor-core kernel (attention_tc.cu): any number of rows.
 size_t tc_workspace_bytes(int64_t rows, int d, int num_sms);
-cudaError_t launch_tc(const Params& p, int64_t rows, int num_sms, cudaStream_t stream);
+cudaError_t launch_tc(const Params& p, bool e4m3, int64_t rows, int num_sms, cudaStream_t stream);
 
 inline ScoreMap score_map(float scale, float softcap) {
     ScoreMap m;

@@ -142,16 +142,25 @@ int device_caps(DeviceCaps* out) {
     return MXFP4_OK;
 }
 
-cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& c) {
-    const cuuint64_t page = cuuint64_t(1) << c.page_shift, d = c.head_dim;
-    const cuuint64_t dims[4] = {d, page, static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)};
-    const cuuint64_t strides[3] = {d * 2, page * d * 2, static_cast<cuuint64_t>(c.page_stride) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page < 128 ? page : 128), 1, 1};
+namespace {
+cudaError_t encode_4d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const cuuint64_t (&dims)[4],
+                      const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
     const cuuint32_t estride[4] = {1, 1, 1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box,
-                                estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = g_encode(map, type, 4, const_cast<void*>(base), dims, strides, box, estride,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& c, bool e4m3) {
+    const cuuint64_t page = cuuint64_t(1) << c.page_shift, d = c.head_dim, e = e4m3 ? 1 : 2;
+    const cuuint32_t rows = static_cast<cuuint32_t>(page < 128 ? page : 128);
+    return encode_4d(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool,
+                     {d, page, static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages)},
+                     {d * e, page * d * e, static_cast<cuuint64_t>(c.page_stride) * e},
+                     {e4m3 ? static_cast<cuuint32_t>(d) : 64u, rows, 1, 1},
+                     e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int encode_weights(CUtensorMap* map, const uint8_t* wq, int64_t rows, int64_t k, int steps, int* is3d) {

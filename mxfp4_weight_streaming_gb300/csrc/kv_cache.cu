@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_accept_kernel(PoolView poo
     pdl_launch_dependents();
     const int b = blockIdx.x;
     int first, n, seq;
-    request_extent(bt, b, pool.page_shift, first, n, seq);
+    request_extent(bt, b, first, n, seq);
     const int start = max(seq - n, 0);
     const int took = min(max(n_accept[b], 0), min(path_len, seq - start));
     if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) lens_out[b] = start + took;

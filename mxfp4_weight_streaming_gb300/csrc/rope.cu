@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
     pdl_launch_dependents();
     const int b = request_of(p.batch, token);
     int first, n, seq;
-    request_extent(p.batch, b, cv.page_shift, first, n, seq);
+    request_extent(p.batch, b, first, n, seq);
     const int i = token - first;
     if (i < 0 || i >= n) return;  // a row of q that belongs to no request
     const int at = seq - n + i;

@@ -66,13 +66,15 @@ CacheView cache_view(const mxfp4_kv_cache_t& c) {
     return v;
 }
 
-BatchView batch_view(const mxfp4_kv_batch_t& b) {
+BatchView batch_view(const mxfp4_kv_batch_t& b, int page_size) {
     BatchView v{};
     v.q_start = b.q_start;
     v.seq_lens = b.seq_lens;
     v.block_table = b.block_table;
     v.table_stride = b.table_stride ? b.table_stride : b.table_width;
     v.table_width = b.table_width;
+    const int64_t room = static_cast<int64_t>(b.table_width) * page_size;
+    v.room = static_cast<int>(room < (int64_t(1) << 30) ? room : (int64_t(1) << 30));
     v.batch = b.batch;
     v.tokens = b.tokens;
     return v;
@@ -158,7 +160,7 @@ int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const in
     a.e4m3 = cache->dtype == MXFP4_KV_E4M3;
     a.factor = factor;
     return launched(
-        mxfp4::launch_rope_append(a, cache_view(*cache), batch_view(*batch), static_cast<cudaStream_t>(stream)));
+        mxfp4::launch_rope_append(a, cache_view(*cache), batch_view(*batch, cache->page_size), static_cast<cudaStream_t>(stream)));
 }
 
 size_t mxfp4_attention_workspace_size(int q_heads, const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* batch) {
@@ -204,7 +206,7 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
     a.scale = scale;
     a.softcap = softcap;
     a.window = window;
-    return launched(mxfp4::launch_attention(a, cache_view(*cache), batch_view(*batch), caps.num_sms,
+    return launched(mxfp4::launch_attention(a, cache_view(*cache), batch_view(*batch, cache->page_size), caps.num_sms,
                                             static_cast<cudaStream_t>(stream)));
 }
 
@@ -277,7 +279,7 @@ int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* ba
     if (!aligned(path, 4) || !aligned(n_accept, 4) || !aligned(lens_out, 4)) return MXFP4_ERR_ALIGN;
     mxfp4::DeviceCaps caps;
     if (int rc = caps_of(&caps)) return rc;
-    return launched(mxfp4::launch_cache_accept(pool_view(*cache), batch_view(*batch), path, path_len, n_accept,
+    return launched(mxfp4::launch_cache_accept(pool_view(*cache), batch_view(*batch, cache->page_size), path, path_len, n_accept,
                                                lens_out, static_cast<cudaStream_t>(stream)));
 }
 

@@ -42,6 +42,7 @@ struct BatchView {
     const int* block_table;  // [batch][table_stride]
     int64_t table_stride;
     int table_width;
+    int room;                // tokens that a row of the table has pages for
     int batch;
     int tokens;
 };
@@ -49,14 +50,12 @@ struct BatchView {
 // Request b's rows of q [first, first + n) and its cache length, clamped to
 // what the arrays and the table can hold, so a wrong length on the device
 // never leads outside a buffer.
-__device__ __forceinline__ void request_extent(const BatchView& bt, int b, int page_shift, int& first, int& n,
-                                               int& seq) {
-    const int lo = min(max(bt.q_start[b], 0), bt.tokens);
-    const int hi = min(max(bt.q_start[b + 1], lo), bt.tokens);
+__device__ __forceinline__ void request_extent(const BatchView& bt, int b, int& first, int& n, int& seq) {
+    const int lo = min(max(__ldg(bt.q_start + b), 0), bt.tokens);
+    const int hi = min(max(__ldg(bt.q_start + b + 1), lo), bt.tokens);
     first = lo;
     n = hi - lo;
-    const int64_t room = static_cast<int64_t>(bt.table_width) << page_shift;
-    seq = static_cast<int>(min(static_cast<int64_t>(max(bt.seq_lens[b], 0)), room));
+    seq = min(max(__ldg(bt.seq_lens + b), 0), bt.room);
 }
 
 // Page of cache index `at` (< table_width << page_shift), or -1 when the

@@ -49,9 +49,10 @@ struct AttentionArgs {
 };
 size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, bool e4m3, int num_sms);
 // K or V pool of a layer as the tensor map attention_tc.cu copies from: (D,
-// page, kv_heads, pages), boxes of 64 elements x min(page, 128) tokens,
-// 128-byte swizzle (capi.cu).
-cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& cache);
+// page, kv_heads, pages): bf16 in boxes of 64 elements x min(page, 128)
+// tokens with the 128-byte swizzle, E4M3 in boxes of D bytes, not swizzled.
+// (capi.cu).
+cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& cache, bool e4m3);
 cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, const BatchView& batch, int num_sms,
                              cudaStream_t stream);
 
