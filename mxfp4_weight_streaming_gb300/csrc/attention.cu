@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     const int64_t share = share_of(cut, total, gridDim.x);
     int64_t unit = share * blockIdx.x;
     const int64_t unit_end = min(unit + share, total);
-    if (threadIdx.x == 0) parts.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) parts.split[blockIdx.x].parts = 0;
 
     while (unit < unit_end) {
         const Item it = locate(cut, p.batch, s_before, unit);
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
         if (!whole && it.tile == 0 && threadIdx.x == 0) {
             const int64_t last = unit + it.tiles - 1;
             parts.split[blockIdx.x] =
-                make_int4(static_cast<int>(last / share) - blockIdx.x + 1, it.b, it.rt, it.head);
+                Split{static_cast<int>(last / share) - static_cast<int>(blockIdx.x) + 1, it.rt * R, rows, it.first, it.head};
         }
         const float vs = E4M3 && cv.v_scale ? cv.v_scale[it.head] : 1.f;
         for (int v = threadIdx.x; v < rows * (D / 4); v += kThreads) {
@@ -526,47 +526,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     pdl_launch_dependents();
 }
 
-// Joins the parts of items that several CTAs shared: block (c, y) takes 32
-// rows of the item that begins in CTA c, and a thread 4 elements of a row.
-// Neighbouring threads are neighbours in the order of the parts: elements of
-// a row, or (parts of attention_tc.cu) rows.
+// Joins the parts of items that several CTAs shared: block (c, y, z) takes
+// rows and elements of the item that begins in CTA c, a thread 4 elements of a
+// row. Neighbouring threads are neighbours in the order of the parts: elements
+// of a row, or (parts of attention_tc.cu) rows. Loads of 8 parts are in flight
+// at a time: the join is all latency.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;
 template <int D, bool E4M3, bool FROM_TC>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(Params p, int ctas) {
     const Cut& cut = p.cut;
-    const int R = 1 << cut.row_shift, rows_here = min(R, 32);
+    const int R = 1 << cut.row_shift;
     pdl_wait_previous();
     pdl_launch_dependents();
     const Parts parts = parts_in(p.ws, ctas, R, D);
-    const int4 sp = parts.split[blockIdx.x];
-    if (sp.x == 0) return;
-    int first, n, seq;
-    request_extent(p.batch, sp.y, first, n, seq);
-    const float vs = E4M3 && p.cache.v_scale ? p.cache.v_scale[sp.w] : 1.f;
-    auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
-    for (int v = threadIdx.x; v < rows_here * (D / 4); v += kJoinThreads) {
-        const int r = blockIdx.y * 32 + (FROM_TC ? v % 32 : v / (D / 4)), d4 = FROM_TC ? v / 32 : v % (D / 4);
-        const int row = sp.z * R + r, tok = cut.by_group.div(row), head = row - tok * cut.group;
-        if (tok >= n) continue;
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int x = 0; x < sp.x; ++x) top = fmaxf(top, parts.ml[slot(x) * R + r].x);
-        const float base = top == -INFINITY ? 0.f : top;
+    const Split sp = parts.split[blockIdx.x];
+    if (sp.parts == 0) return;
+    const int t = threadIdx.x;
+    const int r = FROM_TC ? blockIdx.y * 32 + t % 32 : blockIdx.y * (4 * kJoinThreads / D) + t / (D / 4);
+    if (r >= sp.rows) return;
+    for (int d4 = FROM_TC ? blockIdx.z * 8 + t / 32 : t % (D / 4); d4 < D / 4; d4 += FROM_TC ? 8 * gridDim.z : D / 4) {
+        auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
+        // A running join: what came before is scaled down where a batch's maximum is larger.
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int x = 0; x < sp.x; ++x) {
-            const float2 ml = parts.ml[slot(x) * R + r];
-            const float f = ml.x == top ? 1.f : exp2_fast(ml.x - base);
-            const int64_t at = static_cast<int64_t>(slot(x)) * R * (D / 4) + (FROM_TC ? d4 * R + r : r * (D / 4) + d4);
-            const float4 o = reinterpret_cast<const float4*>(parts.o)[at];
-            sum += f * ml.y;
-            acc.x += f * o.x;
-            acc.y += f * o.y;
-            acc.z += f * o.z;
-            acc.w += f * o.w;
+        float sum = 0.f, top = -INFINITY;
+        for (int x0 = 0; x0 < sp.parts; x0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 o[kJoinBatch];
+            float here = top;
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                ml[x] = make_float2(-INFINITY, 0.f);
+                if (x0 + x >= sp.parts) continue;
+                const int sl = slot(x0 + x);
+                ml[x] = parts.ml[sl * R + r];
+                o[x] = reinterpret_cast<const float4*>(
+                    parts.o)[static_cast<int64_t>(sl) * R * (D / 4) + (FROM_TC ? d4 * R + r : r * (D / 4) + d4)];
+            }
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) here = fmaxf(here, ml[x].x);
+            const float base = here == -INFINITY ? 0.f : here;
+            const float old = top == here ? 1.f : exp2_fast(top - base);
+            acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+            sum *= old;
+            top = here;
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                if (x0 + x >= sp.parts) break;
+                const float f = ml[x].x == here ? 1.f : exp2_fast(ml[x].x - base);
+                sum += f * ml[x].y;
+                acc.x += f * o[x].x;
+                acc.y += f * o[x].y;
+                acc.z += f * o[x].z;
+                acc.w += f * o[x].w;
+            }
         }
-        const int64_t to = static_cast<int64_t>(first + tok) * p.q_heads + sp.w * cut.group + head;
+        const int row = sp.row0 + r, tok = cut.by_group.div(row);
+        const int64_t to = static_cast<int64_t>(sp.first + tok) * p.q_heads + sp.head * cut.group + row - tok * cut.group;
+        const float vs = E4M3 && p.cache.v_scale ? p.cache.v_scale[sp.head] : 1.f;
         const float f = sum == 0.f ? 0.f : vs / sum;
         *reinterpret_cast<uint2*>(p.out + to * D + 4 * d4) =
             make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
@@ -610,8 +627,10 @@ cudaError_t launch_join_d(const PdlLaunch& j, const Params& p, bool from_tc, int
 }  // namespace
 
 cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cudaStream_t stream) {
-    const int blocks = ((1 << p.cut.row_shift) + 31) / 32;
-    PdlLaunch j(dim3(ctas, blocks), dim3(kJoinThreads), 0, stream);
+    const int rows = 1 << p.cut.row_shift, d = p.cache.head_dim, per = 4 * kJoinThreads / d;
+    // With 256 rows an item's blocks are many as it is.
+    const dim3 grid = from_tc ? dim3(ctas, rows / 32, rows == 128 ? d / 32 : 1) : dim3(ctas, (rows + per - 1) / per, 1);
+    PdlLaunch j(grid, dim3(kJoinThreads), 0, stream);
     if (p.cache.head_dim == 64)
         return e4m3 ? launch_join_d<64, true>(j, p, from_tc, ctas) : launch_join_d<64, false>(j, p, from_tc, ctas);
     return e4m3 ? launch_join_d<128, true>(j, p, from_tc, ctas) : launch_join_d<128, false>(j, p, from_tc, ctas);

@@ -169,19 +169,25 @@ __device__ __forceinline__ int64_t share_of(const Cut& c, int64_t total, int cta
 
 // Partial results: two slots per CTA, slot 2c for a part that began before
 // the CTA's run and 2c + 1 for one that begins in it.
+struct alignas(32) Split {
+    int parts;     // 0: there is none
+    int row0, rows;  // its row tile's first row in the request, and its rows
+    int first;     // the request's first row of q
+    int head;      // KV head
+};
 struct Parts {
     float* o;        // [2 ctas], not divided by the sum: [R][D], or from attention_tc.cu [D / 4][R][4]
     float2* ml;      // [2 ctas][R]: running maximum (of log2 scores) and sum
-    int4* split;     // [ctas]: parts of the item that begins in CTA c and ends beyond it (0: none), request, row tile, KV head
+    Split* split;    // [ctas]: the item that begins in CTA c and ends beyond it
 };
 
 __host__ __device__ inline size_t parts_bytes(int ctas, int rows, int d) {
-    return static_cast<size_t>(ctas) * (2 * rows * (d * sizeof(float) + sizeof(float2)) + sizeof(int4));
+    return static_cast<size_t>(ctas) * (2 * rows * (d * sizeof(float) + sizeof(float2)) + sizeof(Split));
 }
 
 __host__ __device__ inline Parts parts_in(void* ws, int ctas, int rows, int d) {
     Parts p;
-    p.split = static_cast<int4*>(ws);
+    p.split = static_cast<Split*>(ws);
     p.ml = reinterpret_cast<float2*>(p.split + ctas);
     p.o = reinterpret_cast<float*>(p.ml + static_cast<size_t>(2) * ctas * rows);
     return p;

@@ -73,7 +73,8 @@ struct alignas(16) Segment {
     int tile0;
     int head;
     int whole, begins; // the whole item; its first tile
-    int b, rt, parts;  // for the join: request, row tile, parts
+    int b;             // request
+    int parts;         // of an item that begins here and ends in another CTA
 };
 
 // Everything the warps tell one another.
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_barrier_init();
     }
     pdl_wait_previous();
-    if (threadIdx.x == 0) parts.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) parts.split[blockIdx.x].parts = 0;
     tc::fence_before_sync();
     const int64_t total = count_units<kTcThreads>(cut, p.batch, threadIdx.x, sh.before);  // ends with a block barrier
     tc::fence_after_sync();
@@ -490,7 +491,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 g.begins = it.tile == 0;
                 g.whole = g.begins && g.steps == it.tiles;
                 g.b = it.b;
-                g.rt = it.rt;
                 const int64_t last = unit + it.tiles - 1;
                 g.parts = g.begins && !g.whole ? static_cast<int>(last >> 31 ? last / share
                                                                              : static_cast<uint32_t>(last) /
@@ -948,7 +948,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     wait_all(sh.pv_done[s], (after[s] - 1) & 1);
             tc::fence_after_sync();
             const int slot = 2 * blockIdx.x + g.begins;
-            if (g.parts && threadIdx.x == 0) parts.split[blockIdx.x] = make_int4(g.parts, g.b, g.rt, g.head);
+            if (g.parts && threadIdx.x == 0)
+                parts.split[blockIdx.x] = Split{g.parts, g.row0, g.rows, g.q0, g.head};
             if (ok) {
                 const int64_t to = static_cast<int64_t>(g.q0 + tok) * p.q_heads + g.head * cut.group + g.row0 + tr -
                                    tok * cut.group;

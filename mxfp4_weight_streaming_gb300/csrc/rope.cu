@@ -6,9 +6,9 @@
 // R of a head's D elements, and becomes
 //   (a cos - b sin, a sin + b cos) * factor.
 // p * inv_freq reaches 1e5 and more, where an fp32 product is off by up to
-// 2^-8 of a radian: the product and its reduction to [-1/2, 1/2] turns are
-// taken in fp64 (one per pair and token, shared by all heads), the sine and
-// cosine in fp32.
+// 2^-8 of a radian: the turns p * inv_freq / 2 pi are taken as a sum of two
+// fp32 numbers (products with their rounding errors, by fma) and reduced to
+// [-1/2, 1/2] before the sine and cosine. One pair's angle serves all heads.
 #include "step_launch.h"
 
 #include "step_common.cuh"
@@ -42,95 +42,137 @@ __device__ __forceinline__ int request_of(const BatchView& bt, int token) {
     return lo;
 }
 
-// One block per (token, share of its heads); a thread takes 8 consecutive
-// elements of one head at a time.
+// Turns of position pos at frequency f, less whole turns: 1/(2 pi) and the
+// products carry their low parts, so the error is about 2^-24 of a turn for
+// any int32 position.
+__device__ __forceinline__ float turns_of(int pos, float f) {
+    constexpr float kInv2Pi = 0.15915494f, kInv2PiLow = 6.4206383e-9f;  // 1/(2 pi) = 0.159154943091895335...
+    const float hi = f * kInv2Pi;
+    const float lo = fmaf(f, kInv2Pi, -hi) + f * kInv2PiLow;
+    float frac = 0.f;
+    // Both parts of the position are exact in fp32.
+    const float part[2] = {static_cast<float>(pos & ~0xfff), static_cast<float>(pos & 0xfff)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float prod = part[i] * hi;
+        frac += (prod - rintf(prod)) + (fmaf(part[i], hi, -prod) + part[i] * lo);
+    }
+    return frac - rintf(frac);
+}
+
+// One block per token. A thread takes 8 consecutive elements of one head at a
+// time; all its loads are under way before the token's request, page and
+// angles are looked up. The partners of 8 elements are another lane's 8 (a
+// head's vectors lie in one warp), or, where R/2 is no multiple of 8, loaded.
 template <bool E4M3>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p) {
-    __shared__ float s_cos[kMaxRotary / 2], s_sin[kMaxRotary / 2];
+    constexpr int kBatch = 5;  // vectors per thread at a time: up to 80 heads of 128 in one go
+    __shared__ __align__(16) float s_cos[kMaxRotary / 2], s_sin[kMaxRotary / 2];
     const int token = blockIdx.x;
     const CacheView& cv = p.cache;
+    const int D = cv.head_dim, vshift = D == 128 ? 4 : 3;  // vectors of a head: 1 << vshift
+    const int heads = p.q_heads + 2 * cv.kv_heads, total = heads << vshift;
+    const int half = p.rotary / 2, hv = half / 8;
+    const bool by_lane = half % 8 == 0;
+    const int lane = threadIdx.x & 31;
     pdl_wait_previous();
     pdl_launch_dependents();
+    const __nv_bfloat16* row = p.qkv + token * p.qkv_stride;
+    uint4 w[kBatch];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = v0 + k * kRopeThreads + threadIdx.x;
+            w[k] = v < total ? *reinterpret_cast<const uint4*>(row + 8 * v) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(0);
     const int b = request_of(p.batch, token);
     int first, n, seq;
     request_extent(p.batch, b, first, n, seq);
     const int i = token - first;
     if (i < 0 || i >= n) return;  // a row of q that belongs to no request
     const int at = seq - n + i;
+    const int page = at >= 0 ? page_of(p.batch, b, at, cv.page_shift, cv.num_pages) : -1;
     const int pos = p.positions ? p.positions[token] : at;
-    const int half = p.rotary / 2;
     for (int j = threadIdx.x; j < half; j += kRopeThreads) {
-        const double turns = static_cast<double>(pos) * static_cast<double>(p.inv_freq[j]) * 0.15915494309189535;
-        const float frac = static_cast<float>(turns - rint(turns));
         float s, c;
-        sincospif(2.f * frac, &s, &c);
+        sincospif(2.f * turns_of(pos, p.inv_freq[j]), &s, &c);
         s_cos[j] = c * p.factor;
         s_sin[j] = s * p.factor;
     }
-    const int page = at >= 0 ? page_of(p.batch, b, at, cv.page_shift, cv.num_pages) : -1;
     __syncthreads();
 
-    const int D = cv.head_dim, vecs = D / 8;
-    const int heads = p.q_heads + 2 * cv.kv_heads;
-    const __nv_bfloat16* row = p.qkv + token * p.qkv_stride;
     const int slot = at & ((1 << cv.page_shift) - 1);
-    const int total = heads * vecs;
-    for (int v = blockIdx.y * kRopeThreads + threadIdx.x; v < total; v += gridDim.y * kRopeThreads) {
-        const int head = v / vecs, d0 = (v % vecs) * 8;
-        const __nv_bfloat16* src = row + head * D;
-        float x[8], o[8];
-        unpack8(*reinterpret_cast<const Bf16x8*>(src + d0), x);
-        if (head >= p.q_heads + cv.kv_heads || d0 >= p.rotary) {
+    for (int v0 = 0; v0 < total; v0 += kBatch * kRopeThreads) {
+        if (v0) load(v0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = x[j];
-        } else if (p.interleaved) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int k = (d0 + j) / 2;
-                const bool in = d0 + j < p.rotary;
-                const float c = in ? s_cos[k] : 1.f, s = in ? s_sin[k] : 0.f;
-                o[j] = x[j] * c - x[j + 1] * s;
-                o[j + 1] = x[j] * s + x[j + 1] * c;
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = v0 + k * kRopeThreads + threadIdx.x;
+            const int head = v >> vshift, vec = v & ((1 << vshift) - 1), d0 = vec * 8;
+            const bool turns = v < total && head < p.q_heads + cv.kv_heads && d0 < p.rotary;
+            float x[8], y[8], o[8];
+            unpack8(*reinterpret_cast<const Bf16x8*>(&w[k]), x);
+            if (!p.interleaved && by_lane && hv) {
+                const int from = vec < hv ? lane + hv : lane - hv;
+                uint4 z;
+                z.x = __shfl_sync(0xffffffffu, w[k].x, from);
+                z.y = __shfl_sync(0xffffffffu, w[k].y, from);
+                z.z = __shfl_sync(0xffffffffu, w[k].z, from);
+                z.w = __shfl_sync(0xffffffffu, w[k].w, from);
+                unpack8(*reinterpret_cast<const Bf16x8*>(&z), y);
             }
-        } else {
-            float y[8];
-            // The partners: 8 consecutive elements R/2 away, 16-byte aligned
-            // unless R/2 is no multiple of 8.
-            const bool low = d0 < half;
-            if (half % 8 == 0) {
-                unpack8(*reinterpret_cast<const Bf16x8*>(src + (low ? d0 + half : d0 - half)), y);
+            if (v >= total) continue;
+            if (!turns) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = x[j];
+            } else if (p.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const int t = (d0 + j) / 2;
+                    const bool in = d0 + j < p.rotary;
+                    const float c = in ? s_cos[t] : 1.f, s = in ? s_sin[t] : 0.f;
+                    o[j] = x[j] * c - x[j + 1] * s;
+                    o[j + 1] = x[j] * s + x[j + 1] * c;
+                }
+            } else if (by_lane) {
+                const bool low = vec < hv;
+                const int t0 = low ? d0 : d0 - half;
+                const float4 *c4 = reinterpret_cast<const float4*>(s_cos + t0),
+                             *s4 = reinterpret_cast<const float4*>(s_sin + t0);
+                const float4 ca = c4[0], cb = c4[1], sa = s4[0], sb = s4[1];
+                const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+                const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = x[j] * c[j] + (low ? -y[j] : y[j]) * s[j];
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int d = d0 + j;
-                    y[j] = d < p.rotary ? __bfloat162float(src[d < half ? d + half : d - half]) : 0.f;
+                    const bool in = d < p.rotary, low = d < half;
+                    const int t = low ? d : d - half;
+                    const float c = in ? s_cos[t] : 1.f, s = in ? s_sin[t] : 0.f;
+                    const float z = in ? __bfloat162float(row[head * D + (low ? d + half : d - half)]) : 0.f;
+                    o[j] = x[j] * c + (low ? -z : z) * s;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d = d0 + j;
-                const bool in = d < p.rotary, lo = d < half;
-                const int k = lo ? d : d - half;
-                const float c = in ? s_cos[k] : 1.f, s = in ? s_sin[k] : 0.f;
-                o[j] = lo ? x[j] * c - y[j] * s : x[j] * c + y[j] * s;
+            if (head < p.q_heads) {
+                *reinterpret_cast<Bf16x8*>(p.q_out + (static_cast<int64_t>(token) * p.q_heads + head) * D + d0) = pack8(o);
+                continue;
             }
-        }
-        if (head < p.q_heads) {
-            *reinterpret_cast<Bf16x8*>(p.q_out + (static_cast<int64_t>(token) * p.q_heads + head) * D + d0) = pack8(o);
-            continue;
-        }
-        if (page < 0) continue;
-        const bool is_v = head >= p.q_heads + cv.kv_heads;
-        const int kh = head - p.q_heads - (is_v ? cv.kv_heads : 0);
-        const int64_t to = page * cv.page_stride + ((static_cast<int64_t>(kh) << cv.page_shift) + slot) * D + d0;
-        if constexpr (E4M3) {
-            const float* sc = is_v ? cv.v_scale : cv.k_scale;
-            const float scale = sc ? sc[kh] : 1.f;
+            if (page < 0) continue;
+            const bool is_v = head >= p.q_heads + cv.kv_heads;
+            const int kh = head - p.q_heads - (is_v ? cv.kv_heads : 0);
+            const int64_t to = page * cv.page_stride + ((static_cast<int64_t>(kh) << cv.page_shift) + slot) * D + d0;
+            if constexpr (E4M3) {
+                const float* sc = is_v ? cv.v_scale : cv.k_scale;
+                const float scale = sc ? sc[kh] : 1.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = o[j] / scale;
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? cv.v : cv.k) + to) = pack8_e4m3(o);
-        } else {
-            *reinterpret_cast<Bf16x8*>(static_cast<__nv_bfloat16*>(is_v ? cv.v : cv.k) + to) = pack8(o);
+                for (int j = 0; j < 8; ++j) o[j] = o[j] / scale;
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? cv.v : cv.k) + to) = pack8_e4m3(o);
+            } else {
+                *reinterpret_cast<Bf16x8*>(static_cast<__nv_bfloat16*>(is_v ? cv.v : cv.k) + to) = pack8(o);
+            }
         }
     }
 }

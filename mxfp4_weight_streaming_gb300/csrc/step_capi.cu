@@ -132,7 +132,7 @@ int mxfp4_residual_norm(const void* x, const void* residual, int64_t tokens, int
     a.eps = eps;
     a.weight_offset = weight_offset;
     a.layer = layer != 0;
-    return launched(mxfp4::launch_residual_norm(a, static_cast<cudaStream_t>(stream)));
+    return launched(mxfp4::launch_residual_norm(a, caps.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const int32_t* positions,

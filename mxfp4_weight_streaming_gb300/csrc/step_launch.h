@@ -18,7 +18,7 @@ struct ResidualNormArgs {
     float scale, eps, weight_offset;
     bool layer;
 };
-cudaError_t launch_residual_norm(const ResidualNormArgs& a, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, int num_sms, cudaStream_t stream);
 
 struct RopeArgs {
     const void* qkv;  // bf16 rows of (q_heads + 2 kv_heads) * head_dim, qkv_stride elements apart
