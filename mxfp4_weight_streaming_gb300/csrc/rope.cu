@@ -25,7 +25,7 @@ struct RopeParams {
     const int* positions;
     const float* inv_freq;
     __nv_bfloat16* q_out;
-    int q_heads, rotary, interleaved;
+    int q_heads, rotary;
     float factor;
     CacheView cache;
     BatchView batch;
@@ -60,13 +60,19 @@ __device__ __forceinline__ float turns_of(int pos, float f) {
     return frac - rintf(frac);
 }
 
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = a * c - b * s;
+    b = a * s + b * c;
+    a = x;
+}
+
 // One block per token. A thread takes 8 consecutive elements of one head at a
 // time; all its loads are under way before the token's request, page and
 // angles are looked up. The partners of 8 elements are another lane's 8 (a
 // head's vectors lie in one warp), or, where R/2 is no multiple of 8, loaded.
-template <bool E4M3>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p) {
-    constexpr int kBatch = 5;  // vectors per thread at a time: up to 80 heads of 128 in one go
+template <bool E4M3, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(RopeParams p) {
+    constexpr int kBatch = 5;  // vectors per thread at a time: 80 heads of 128 in one go
     __shared__ __align__(16) float s_cos[kMaxRotary / 2], s_sin[kMaxRotary / 2];
     const int token = blockIdx.x;
     const CacheView& cv = p.cache;
@@ -110,68 +116,72 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
         for (int k = 0; k < kBatch; ++k) {
             const int v = v0 + k * kRopeThreads + threadIdx.x;
             const int head = v >> vshift, vec = v & ((1 << vshift) - 1), d0 = vec * 8;
-            const bool turns = v < total && head < p.q_heads + cv.kv_heads && d0 < p.rotary;
-            float x[8], y[8], o[8];
-            unpack8(*reinterpret_cast<const Bf16x8*>(&w[k]), x);
-            if (!p.interleaved && by_lane && hv) {
+            uint4 z;
+            if (!INTERLEAVED && by_lane) {
                 const int from = vec < hv ? lane + hv : lane - hv;
-                uint4 z;
                 z.x = __shfl_sync(0xffffffffu, w[k].x, from);
                 z.y = __shfl_sync(0xffffffffu, w[k].y, from);
                 z.z = __shfl_sync(0xffffffffu, w[k].z, from);
                 z.w = __shfl_sync(0xffffffffu, w[k].w, from);
-                unpack8(*reinterpret_cast<const Bf16x8*>(&z), y);
             }
             if (v >= total) continue;
-            if (!turns) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = x[j];
-            } else if (p.interleaved) {
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const int t = (d0 + j) / 2;
-                    const bool in = d0 + j < p.rotary;
-                    const float c = in ? s_cos[t] : 1.f, s = in ? s_sin[t] : 0.f;
-                    o[j] = x[j] * c - x[j + 1] * s;
-                    o[j + 1] = x[j] * s + x[j + 1] * c;
-                }
-            } else if (by_lane) {
+            const bool is_q = head < p.q_heads, is_v = head >= p.q_heads + cv.kv_heads;
+            const bool turns = !is_v && d0 < p.rotary;
+            float o[8];
+            if (turns || E4M3) unpack8(*reinterpret_cast<const Bf16x8*>(&w[k]), o);
+            if (turns && (INTERLEAVED ? d0 + 8 <= p.rotary : by_lane)) {
+                // 4 neighbouring pairs' angles, or 8 in the half's order.
                 const bool low = vec < hv;
-                const int t0 = low ? d0 : d0 - half;
+                const int t0 = INTERLEAVED ? d0 / 2 : low ? d0 : d0 - half;
                 const float4 *c4 = reinterpret_cast<const float4*>(s_cos + t0),
                              *s4 = reinterpret_cast<const float4*>(s_sin + t0);
-                const float4 ca = c4[0], cb = c4[1], sa = s4[0], sb = s4[1];
-                const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-                const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+                if (INTERLEAVED) {
+                    const float4 c = c4[0], s = s4[0];
+                    turn(o[0], o[1], c.x, s.x);
+                    turn(o[2], o[3], c.y, s.y);
+                    turn(o[4], o[5], c.z, s.z);
+                    turn(o[6], o[7], c.w, s.w);
+                } else {
+                    float y[8];
+                    unpack8(*reinterpret_cast<const Bf16x8*>(&z), y);
+                    const float4 ca = c4[0], cb = c4[1], sa = s4[0], sb = s4[1];
+                    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+                    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+                    const float sign = low ? -1.f : 1.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = x[j] * c[j] + (low ? -y[j] : y[j]) * s[j];
-            } else {
+                    for (int j = 0; j < 8; ++j) o[j] = fmaf(o[j], c[j], sign * y[j] * s[j]);
+                }
+            } else if (turns) {  // a rotary dimension that ends inside 8 elements, or whose half does
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int d = d0 + j;
-                    const bool in = d < p.rotary, low = d < half;
-                    const int t = low ? d : d - half;
-                    const float c = in ? s_cos[t] : 1.f, s = in ? s_sin[t] : 0.f;
-                    const float z = in ? __bfloat162float(row[head * D + (low ? d + half : d - half)]) : 0.f;
-                    o[j] = x[j] * c + (low ? -z : z) * s;
+                    if (d >= p.rotary) continue;
+                    const bool low = INTERLEAVED ? !(d & 1) : d < half;
+                    const int t = INTERLEAVED ? d >> 1 : low ? d : d - half;
+                    const int step = INTERLEAVED ? 1 : half;
+                    const float y = __bfloat162float(row[head * D + (low ? d + step : d - step)]);
+                    o[j] = o[j] * s_cos[t] + (low ? -y : y) * s_sin[t];
                 }
             }
-            if (head < p.q_heads) {
-                *reinterpret_cast<Bf16x8*>(p.q_out + (static_cast<int64_t>(token) * p.q_heads + head) * D + d0) = pack8(o);
+            if (is_q) {
+                uint4* to = reinterpret_cast<uint4*>(p.q_out) + static_cast<int64_t>(token) * (p.q_heads << vshift) + v;
+                if (turns) *reinterpret_cast<Bf16x8*>(to) = pack8(o);
+                else *to = w[k];
                 continue;
             }
             if (page < 0) continue;
-            const bool is_v = head >= p.q_heads + cv.kv_heads;
             const int kh = head - p.q_heads - (is_v ? cv.kv_heads : 0);
-            const int64_t to = page * cv.page_stride + ((static_cast<int64_t>(kh) << cv.page_shift) + slot) * D + d0;
+            const int64_t to = page * cv.page_stride + ((kh << cv.page_shift) + slot) * D + d0;
             if constexpr (E4M3) {
                 const float* sc = is_v ? cv.v_scale : cv.k_scale;
-                const float scale = sc ? sc[kh] : 1.f;
+                const float inv = sc ? __frcp_rn(sc[kh]) : 1.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = o[j] / scale;
+                for (int j = 0; j < 8; ++j) o[j] *= inv;
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? cv.v : cv.k) + to) = pack8_e4m3(o);
             } else {
-                *reinterpret_cast<Bf16x8*>(static_cast<__nv_bfloat16*>(is_v ? cv.v : cv.k) + to) = pack8(o);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? cv.v : cv.k) + to);
+                if (turns) *reinterpret_cast<Bf16x8*>(dst) = pack8(o);
+                else *dst = w[k];
             }
         }
     }
@@ -189,13 +199,15 @@ cudaError_t launch_rope_append(const RopeArgs& a, const CacheView& cache, const 
     p.q_out = static_cast<__nv_bfloat16*>(a.q_out);
     p.q_heads = a.q_heads;
     p.rotary = a.rotary_dim;
-    p.interleaved = a.interleaved;
     p.factor = a.factor;
     p.cache = cache;
     p.batch = batch;
     PdlLaunch l(dim3(batch.tokens, 1), dim3(kRopeThreads), 0, stream);
-    return a.e4m3 ? cudaLaunchKernelEx(&l.cfg, rope_append_kernel<true>, p)
-                  : cudaLaunchKernelEx(&l.cfg, rope_append_kernel<false>, p);
+    if (a.interleaved)
+        return a.e4m3 ? cudaLaunchKernelEx(&l.cfg, rope_append_kernel<true, true>, p)
+                      : cudaLaunchKernelEx(&l.cfg, rope_append_kernel<false, true>, p);
+    return a.e4m3 ? cudaLaunchKernelEx(&l.cfg, rope_append_kernel<true, false>, p)
+                  : cudaLaunchKernelEx(&l.cfg, rope_append_kernel<false, false>, p);
 }
 
 }  // namespace mxfp4
