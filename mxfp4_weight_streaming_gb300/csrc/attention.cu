@@ -29,8 +29,14 @@ constexpr int kKeys = 16;                // keys per warp and step
 constexpr int kKeyTile = kKeys * kWarps;  // keys per CTA and step
 constexpr int kKeyShift = 6;
 static_assert(kKeyTile == 1 << kKeyShift);
-constexpr int kRingBytes = 24 * 1024;    // per warp
-constexpr int kCtasPerSm = 2;
+// CTAs per SM, and the ring of a warp. The kernel is bound by the latency of
+// its chains (load, score, maximum, product): with 16 rows and K rows of up to
+// 128 bytes registers and rings leave room for three CTAs (64 requests of
+// 6,000 tokens, E4M3, D = 128: 173 us with two, 142 with three, 200 with four,
+// whose rings are too short).
+__host__ __device__ constexpr bool three_ctas(int d, bool e4m3, int mt) { return mt == 1 && d * (e4m3 ? 1 : 2) <= 128; }
+__host__ __device__ constexpr int ctas_per_sm(int d, bool e4m3, int mt) { return three_ctas(d, e4m3, mt) ? 3 : 2; }
+__host__ __device__ constexpr int ring_bytes(int d, bool e4m3, int mt) { return three_ctas(d, e4m3, mt) ? 16384 : 24576; }
 // A running maximum is raised only when a score exceeds it by more than this
 // (log2): probabilities stay below 2^8, and the accumulators are seldom
 // rescaled.
@@ -82,13 +88,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Shared-memory address of 16-byte chunk c of row r: chunks are XORed with
 // the row so that 8 rows of one column of chunks cover all banks.
+template <int CH>
+__device__ __forceinline__ int swizzle(int r) {
+    return CH >= 8 ? (r & 7) : ((r >> 1) & (CH - 1));
+}
 template <int RB>
 __device__ __forceinline__ uint32_t at(uint32_t base, int r, int c) {
-    constexpr int CH = RB / 16;
-    const int x = CH >= 8 ? (r & 7) : ((r >> 1) & (CH - 1));
-    return base + r * RB + ((c ^ x) << 4);
+    return base + r * RB + ((c ^ swizzle<RB / 16>(r)) << 4);
 }
 
 // Whether a 16-byte chunk of a V row holds an infinity or a NaN.
@@ -119,12 +131,13 @@ __device__ __forceinline__ float v_element(uint32_t vst, int r, int d) {
 }
 
 template <int D, bool E4M3, int MT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, E4M3, MT)) attention_rows_kernel(Params p) {
     constexpr int R = 16 * MT;                 // rows of a row tile
     constexpr int RB = D * (E4M3 ? 1 : 2);     // bytes of a K or V row
     constexpr int CH = RB / 16;
     constexpr int STAGE = 2 * kKeys * RB;      // K rows, then V rows
-    constexpr int STAGES = kRingBytes / STAGE < 8 ? kRingBytes / STAGE : 8;
+    constexpr int RING = ring_bytes(D, E4M3, MT);
+    constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;
     constexpr int KK = D / 16;
     static_assert(STAGES >= 3 && R * D * 4 <= STAGES * STAGE, "ring too small for the join");
 
@@ -134,6 +147,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * (STAGES * STAGE);
+    // A lane copies chunk lane % CH of rows lane / CH, + 32 / CH, ...: the row's
+    // share of the address and of the XOR split into a lane's and a step's part.
+    const uint32_t lane_at_row = (lane / CH) * RB;
+    const int lane_chunk = (lane % CH) ^ swizzle<CH>(lane / CH);
     float* const join = reinterpret_cast<float*>(smem);  // [warp][R][D] over the rings
     constexpr int kJoinStride = STAGES * STAGE / 4;
     const CacheView& cv = p.cache;
@@ -166,15 +183,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attention_rows_kernel(Pa
                 const int key = key0 + step * kKeyTile;
                 const uint32_t dst = ring + (step % STAGES) * STAGE;
                 const int64_t off = (page < 0 ? 0 : page) * cv.page_stride + (head_off + (key & page_mask)) * D;
-                const char* kp = static_cast<const char*>(cv.k) + off * (E4M3 ? 1 : 2);
-                const char* vp = static_cast<const char*>(cv.v) + off * (E4M3 ? 1 : 2);
+                const char* kp = static_cast<const char*>(cv.k) + off * (E4M3 ? 1 : 2) + lane * 16;
+                const char* vp = static_cast<const char*>(cv.v) + off * (E4M3 ? 1 : 2) + lane * 16;
+                // The rows of 16 keys are contiguous: copy i takes 512 bytes on.
+                const bool all = page >= 0 && key >= it.begin && key + kKeys <= it.end;
+                if (all) {
 #pragma unroll
-                for (int i = 0; i < kKeys * CH / 32; ++i) {
-                    const int idx = i * 32 + lane, r = idx / CH, c = idx % CH;
-                    const bool valid = page >= 0 && key + r >= it.begin && key + r < it.end;
-                    const int64_t o = valid ? r * RB + c * 16 : 0;
-                    cp_async16(at<RB>(dst, r, c), valid ? kp + o : static_cast<const char*>(cv.k), valid);
-                    cp_async16(at<RB>(dst + kKeys * RB, r, c), valid ? vp + o : static_cast<const char*>(cv.v), valid);
+                    for (int i = 0; i < kKeys * CH / 32; ++i) {
+                        const uint32_t to = dst + lane_at_row + i * 512 + ((lane_chunk ^ swizzle<CH>(i * (32 / CH))) << 4);
+                        cp_async16_all(to, kp + i * 512);
+                        cp_async16_all(to + kKeys * RB, vp + i * 512);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kKeys * CH / 32; ++i) {
+                        const int r = i * (32 / CH) + lane / CH;
+                        const bool valid = page >= 0 && key + r >= it.begin && key + r < it.end;
+                        const uint32_t to = dst + lane_at_row + i * 512 + ((lane_chunk ^ swizzle<CH>(i * (32 / CH))) << 4);
+                        cp_async16(to, valid ? kp + i * 512 : static_cast<const char*>(cv.k), valid);
+                        cp_async16(to + kKeys * RB, valid ? vp + i * 512 : static_cast<const char*>(cv.v), valid);
+                    }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(Params p, 
 
 template <int D, bool E4M3, int MT>
 cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
-    constexpr int smem = kWarps * kRingBytes;
+    constexpr int smem = kWarps * ring_bytes(D, E4M3, MT);
     static thread_local int ready_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -641,7 +669,8 @@ cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cuda
 size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q, bool e4m3, int num_sms) {
     const int64_t rows = static_cast<int64_t>(max_q) * (q_heads / kv_heads);
     if (attn::use_tc(rows, e4m3)) return attn::tc_workspace_bytes(rows, head_dim, num_sms);
-    return attn::parts_bytes(attn::kCtasPerSm * num_sms, rows <= 16 ? 16 : 32, head_dim);
+    const int mt = rows <= 16 ? 1 : 2;
+    return attn::parts_bytes(attn::ctas_per_sm(head_dim, e4m3, mt) * num_sms, 16 * mt, head_dim);
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, const BatchView& batch, int num_sms,
@@ -674,7 +703,7 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
     const int mt = rows <= 16 ? 1 : 2;
     p.cut.row_shift = mt == 1 ? 4 : 5;
     p.cut.key_shift = attn::kKeyShift;
-    const int ctas = attn::kCtasPerSm * num_sms;
+    const int ctas = attn::ctas_per_sm(cache.head_dim, a.e4m3, mt) * num_sms;
     return cache.head_dim == 64 ? attn::launch_d<64>(p, a.e4m3, mt, ctas, stream)
                                 : attn::launch_d<128>(p, a.e4m3, mt, ctas, stream);
 }

@@ -22,10 +22,9 @@
 //             Q K^T, V as it lies in memory an N-major B operand of P V.
 //             Warp 9 finds the CTA's parts of items and tells the others
 //   11        copies the rows of q
-//   10, 11    E4M3 caches (warp 9 copies V too): turn the copied bytes into
-//             f16 tiles of the ring (exact; the scales go to the scores and
-//             the outputs), and q into f16, each row by a power of two that
-//             keeps it in range
+//   12-15     E4M3 caches only: turn the copied bytes into f16 tiles of the
+//             ring (exact; the scales go to the scores and the outputs), and
+//             q into f16, each row by a power of two that keeps it in range
 // Operands are bf16, with an E4M3 cache f16 (probabilities too).
 //
 // A row's running maximum is raised only when a score exceeds it by 2^8, so
@@ -42,9 +41,10 @@ namespace mxfp4 {
 namespace attn {
 namespace {
 
-constexpr int kTcThreads = 384;
+// 12 warps, and 4 more where an E4M3 cache is to be converted.
+__host__ __device__ constexpr int tc_threads(bool e4m3) { return e4m3 ? 512 : 384; }
 constexpr int kTcKeys = 128;   // keys per tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kLoadVWarp = 10, kConvertWarp = 12;
 constexpr float kTcSlack = 8.f;
 
 template <int D, bool SPLIT, bool E4M3>
@@ -54,9 +54,9 @@ struct Layout {
     static constexpr int kQ = (SPLIT ? 1 : 2) * kTile;
     // bf16: 5 tiles of 32 KB, or 8 of 16 KB: three or more in flight beside
     // the two in use. E4M3: the tiles in flight are the raw ones.
-    static constexpr int kSlots = D == 128 ? (E4M3 ? 4 : 5) : (E4M3 ? 6 : 8);
+    static constexpr int kSlots = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 5 : 8);
     static constexpr int kRawTile = E4M3 ? kTcKeys * D : 0;
-    static constexpr int kRawSlots = !E4M3 ? 1 : D == 64 ? 4 : SPLIT ? 3 : 2;
+    static constexpr int kRawSlots = !E4M3 ? 1 : D == 64 ? 8 : SPLIT ? 5 : 4;
     static constexpr int kRing = kQ;               // offsets
     static constexpr int kRaw = kRing + kSlots * kTile;
     static constexpr int kBytes = kRaw + kRawSlots * kRawTile + 1024;  // and alignment
@@ -81,7 +81,7 @@ struct alignas(16) Segment {
 template <bool SPLIT, bool E4M3>
 struct Shared {
     int64_t before[kGroups + 1];
-    uint64_t kv_full[8], kv_empty[8], raw_full[4], raw_empty[4], patch, q_full, q_empty, s_full[2], p_full[2][2],
+    uint64_t kv_full[8], kv_empty[8], raw_full[8], raw_empty[8], patch, q_full, q_empty, s_full[2], p_full[2][2],
         pv_done[2], vote[2], meet, drain, seg_full[2], seg_empty[2];
     Segment seg[2];
     float m[2][SPLIT ? 128 : 1], l[2][SPLIT ? 128 : 1];  // of the two streams' rows
@@ -412,7 +412,7 @@ struct Loader {
 };
 
 template <int D, bool SPLIT, bool CAP, bool E4M3>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(E4M3), 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ Params p) {
     using L = Layout<D, SPLIT, E4M3>;
@@ -434,15 +434,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
         sh.abort = 0;
         for (int i = 0; i < 8; ++i) {
-            mbar_init(smem_addr(&sh.kv_full[i]), E4M3 ? 64 : 1);
+            mbar_init(smem_addr(&sh.kv_full[i]), E4M3 ? 128 : 1);
             mbar_init(smem_addr(&sh.kv_empty[i]), 1);
-        }
-        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&sh.raw_full[i]), 1);
-            mbar_init(smem_addr(&sh.raw_empty[i]), 64);
+            mbar_init(smem_addr(&sh.raw_empty[i]), 128);
         }
         mbar_init(smem_addr(&sh.patch), 1);
-        mbar_init(smem_addr(&sh.q_full), E4M3 ? 64 : 32);
+        mbar_init(smem_addr(&sh.q_full), E4M3 ? 128 : 32);
         mbar_init(smem_addr(&sh.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&sh.s_full[s]), 1);
@@ -451,7 +449,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_addr(&sh.pv_done[s]), 1);
             mbar_init(smem_addr(&sh.vote[s]), 128);
             mbar_init(smem_addr(&sh.seg_full[s]), 1);
-            mbar_init(smem_addr(&sh.seg_empty[s]), 11);  // warps
+            mbar_init(smem_addr(&sh.seg_empty[s]), E4M3 ? 14 : 11);  // warps
             sh.bad[s] = sh.skip[s] = 0;
         }
         mbar_init(smem_addr(&sh.meet), 256);
@@ -461,14 +459,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_wait_previous();
     if (threadIdx.x == 0) parts.split[blockIdx.x].parts = 0;
     tc::fence_before_sync();
-    const int64_t total = count_units<kTcThreads>(cut, p.batch, threadIdx.x, sh.before);  // ends with a block barrier
+    const int64_t total = count_units<tc_threads(E4M3)>(cut, p.batch, threadIdx.x, sh.before);  // ends with a block barrier
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
 
     // 384 threads start with 168 registers each; the two groups that hold a
-    // row of scores per thread take 200, the third keeps 104 (the sum is the same).
+    // row of scores per thread take 200, the third keeps 104. 512 threads start
+    // with 128: 168, and 88 for the others. (The sums are the same.)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kLoadWarp) {
         const int64_t share = share_of(cut, total, gridDim.x);
         int64_t unit = share * blockIdx.x;
@@ -510,29 +510,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (g.steps == 0) break;
             ld.begin_segment(g);
             const int n = __shfl_sync(0xffffffffu, g.steps, 0);
-            if constexpr (E4M3) {  // both kinds of tiles, in ring order
-                int pk0 = ld.page_for(0), pk1 = ld.page_for(1), pv0 = pk0, pv1 = pk1;
+            // K; the other load warp copies V.
+            int p0 = ld.page_for(0), p1 = ld.page_for(1);
 #pragma unroll 1
-                for (int i = 0; i < 2 * n && ld.ok; ++i) {
-                    bool v;
-                    const int step = ring_order<SPLIT>(i, n, v);
-                    ld.tile(v ? &vmap : &kmap, used + i, step, v, v ? pv0 : pk0);
-                    if (v) {
-                        pv0 = pv1;
-                        pv1 = ld.page_for(step + 2);
-                    } else {
-                        pk0 = pk1;
-                        pk1 = ld.page_for(step + 2);
-                    }
-                }
-            } else {  // K; the other load warp copies V
-                int p0 = ld.page_for(0), p1 = ld.page_for(1);
-#pragma unroll 1
-                for (int j = 0; j < n && ld.ok; ++j) {
-                    ld.tile(&kmap, used + k_place<SPLIT>(j), j, false, p0);
-                    p0 = p1;
-                    p1 = ld.page_for(j + 2);
-                }
+            for (int j = 0; j < n && ld.ok; ++j) {
+                ld.tile(&kmap, used + k_place<SPLIT>(j), j, false, p0);
+                p0 = p1;
+                p1 = ld.page_for(j + 2);
             }
             used += 2 * n;
         }
@@ -642,7 +626,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             while (!mbar_try_wait(smem_addr(&sh.drain), 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (!E4M3 && warp == kConvertWarp) {
+    } else if (warp == kLoadVWarp) {
         Loader<D, SPLIT, E4M3> ld(p, sh, wait, base, lane);
         uint32_t turn = 0, used = 0;
         Segment g;
@@ -681,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_proxy_async_shared();
             mbar_arrive(smem_addr(&sh.q_full));
         }
-    } else {
+    } else if (warp >= kConvertWarp) {
         uint32_t turn = 0, count = 0;
         bool ok = true;
         Segment g;
@@ -694,17 +678,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) return;
             int lo, hi;
             tile_rows(g, step, lo, hi);
-            const uint32_t src = base + L::kRaw + rs * L::kRawTile, dst = base + L::kRing + slot * L::kTile;
-#pragma unroll 4
-            for (int i = t; i < kTcKeys * (D / 16); i += 64) {
-                const int r = i / (D / 16), c = i % (D / 16);
-                uint4 w = lds128(src + i * 16);
-                if (r < lo || r >= hi) w = make_uint4(0, 0, 0, 0);
+            // A thread takes the same 16 elements of every 2048 / D-th row, so its
+            // addresses (and its place in the swizzle) move by constants.
+            constexpr int kRows = 2048 / D, kTurns = kTcKeys / kRows;
+            const int r0 = t / (D / 16), c = t % (D / 16), x = 2 * (c & 3);
+            const uint32_t src = base + L::kRaw + rs * L::kRawTile + t * 16;
+            const uint32_t dst = base + L::kRing + slot * L::kTile + (c >> 2) * L::kHalf + r0 * 128;
+            const uint32_t d0 = dst + ((x ^ (r0 & 7)) << 4), d1 = dst + (((x + 1) ^ (r0 & 7)) << 4);
+            const bool whole = lo == 0 && hi == kTcKeys;
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                uint4 w = lds128(src + k * 2048);
+                if (!whole && (r0 + k * kRows < lo || r0 + k * kRows >= hi)) w = make_uint4(0, 0, 0, 0);
                 const uint2 a = e4m3x4_to_f16x4(w.x), b = e4m3x4_to_f16x4(w.y), d = e4m3x4_to_f16x4(w.z),
                             e = e4m3x4_to_f16x4(w.w);
-                const uint32_t row = dst + (c >> 2) * L::kHalf + r * 128, x = 2 * (c & 3);
-                sts128(row + ((x ^ (r & 7)) << 4), a.x, a.y, b.x, b.y);
-                sts128(row + (((x + 1) ^ (r & 7)) << 4), d.x, d.y, e.x, e.y);
+                sts128(d0 + k * kRows * 128, a.x, a.y, b.x, b.y);
+                sts128(d1 + k * kRows * 128, d.x, d.y, e.x, e.y);
             }
             fence_proxy_async_shared();
             mbar_arrive(smem_addr(&sh.raw_empty[rs]));
@@ -716,7 +705,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ok = ok && (turn < 2 || mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
             if (!ok) return;
 #pragma unroll 1
-            for (int r = t; r < R; r += 64) {
+            for (int r = t; r < R; r += 128) {
                 const uint4* src = reinterpret_cast<const uint4*>(q_row(p, g, r));
                 const uint32_t row = base + (r >> 7) * L::kTile + (r & 127) * 128;
                 float top = 0.f;
@@ -755,7 +744,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t st = tmem + wg * 128 + lane_at;      // S, then P
@@ -1027,7 +1017,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, 
         if (e != cudaSuccess) return e;
         ready_device = dev;
     }
-    PdlLaunch l(dim3(ctas), dim3(kTcThreads), smem, stream);
+    PdlLaunch l(dim3(ctas), dim3(tc_threads(E4M3)), smem, stream);
     return cudaLaunchKernelEx(&l.cfg, attention_tc_kernel<D, SPLIT, CAP, E4M3>, k, v, p);
 }
 
