@@ -355,7 +355,7 @@ struct Loader {
     __device__ __forceinline__ int page_for(int step) const {
         const int key = key_base + step * kTcKeys + lane * box_rows;
         int pg = -1;
-        if (step < steps && lane < boxes && key < end && key + box_rows > begin) pg = __ldg(table + (key >> page_shift));
+        if (step < steps && lane < boxes && key < end && key + box_rows > begin) pg = table[key >> page_shift];
         return static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.cache.num_pages) ? pg : p.cache.num_pages;
     }
 
@@ -364,6 +364,7 @@ struct Loader {
         const uint32_t slot = n % kRingSlots, turn = n / kRingSlots;
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * slot, (turn & 1) ^ 1, wait));
         if (!ok) return;
+        if (withhold_stage(n)) return;  // test builds only
         const int key0 = key_base + step * kTcKeys;
         // Rows of V that hold no key of this item but lie in a page that
         // does: whatever is there must not meet the products (0 * NaN).

@@ -214,3 +214,34 @@ def test_pages_beyond_32_bit_offsets():
     kp[order], vp[order] = pg.kp[pg.table[0].long()], pg.vp[pg.table[0].long()]
     pg.kp, pg.vp, pg.table = kp, vp, order.to(torch.int32)[None].contiguous()
     run(pg, [2], 16, what="far pages")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("news,heads,cap", [([8], 8, 0.0), ([200], 8, 30.0)])
+def test_a_wait_that_runs_out_is_reported(dtype, news, heads, cap):
+    """On a test-only build whose first K tile never arrives (and a limit of
+    1 ms): the call ends, the status says so, and the product library's next
+    call is right."""
+    import ctypes
+
+    from mxfp4_weight_streaming_gb300 import build
+    mx = lib()
+    path = build.build_test_variant("withhold", ["MXFP4_TEST_WITHHOLD_STAGE", "MXFP4_WAIT_LIMIT_NS=1000000ull"])
+    other = ctypes.CDLL(path)
+    P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    other.mxfp4_attention.argtypes = [P, ctypes.c_int64, I, P, P, F, F, I, P, P, P, P, ctypes.c_size_t, P]
+    other.mxfp4_last_device_status.argtypes = [P]
+    pg = Paged(3, [news[0] + 700], 1, 128, 32, dtype)
+    q = randn(gen(1), news[0], heads, 128)
+    cache, batch = pg.cache(mx), pg.batch(mx, news)
+    ws, out = mx.attention_workspace(heads, cache, batch), torch.empty_like(q)
+    stream = torch.cuda.current_stream().cuda_stream
+    rc = other.mxfp4_attention(q.data_ptr(), q.stride(0), heads, cache.ref, batch.ref, 0.1, cap, 0, None, out.data_ptr(),
+                               None, ws.data_ptr(), ws.numel(), stream)
+    assert rc == mx.MXFP4_OK
+    assert other.mxfp4_last_device_status(stream) == mx.MXFP4_ERR_TIMEOUT
+    assert other.mxfp4_last_device_status(stream) == mx.MXFP4_OK
+    out = mx.attention(q, cache, batch, scale=0.1, softcap=cap, workspace=ws)
+    assert mx.last_device_status() == mx.MXFP4_OK
+    ref, _, mag = attention_ref(pg, q, 0.1, cap)
+    check(out, ref, attention_bound(ref, mag, dtype), "after the timeout")
