@@ -229,6 +229,7 @@ __device__ __noinline__ void add_tile_by_rows(uint32_t ot, uint32_t pt, uint32_t
             uint32_t pair;
             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(pair) : "r"(pt + k2) : "memory");
             tc::tmem_wait_ld();
+            asm volatile("" : "+r"(pair)::"memory");
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float f = half_of<F16>(pair, h);
@@ -355,7 +356,7 @@ struct Loader {
     __device__ __forceinline__ int page_for(int step) const {
         const int key = key_base + step * kTcKeys + lane * box_rows;
         int pg = -1;
-        if (step < steps && lane < boxes && key < end && key + box_rows > begin) pg = table[key >> page_shift];
+        if (step < steps && lane < boxes && key < end && key + box_rows > begin) pg = load_word(table + (key >> page_shift));
         return static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.cache.num_pages) ? pg : p.cache.num_pages;
     }
 
@@ -797,6 +798,8 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_load32(st + c * 32, s + c * 32);
                 tc::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) loaded32(s + c * 32);
                 if constexpr (CAP) {
                     // ScoreMap's formula, two scores an instruction where there is one.
                     const uint64_t cmul = f32x2_pack(mul, mul), one = f32x2_pack(1.f, 1.f);
@@ -853,14 +856,16 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
                     if (jj) {  // the first product of a segment overwrites O
                         if (!wait_all(sh.pv_done[wg], (turn - 1) & 1)) break;
                         tc::fence_after_sync();
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tc::TmemLd<16>::load(ot + c * 16, o);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_load32(ot + c, o);
                             tc::tmem_wait_ld();
+                            loaded32(o);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tc::tmem_store16(ot + c * 16, o);
+                            for (int x = 0; x < 32; ++x) o[x] *= f;
+                            tc::tmem_store16(ot + c, *reinterpret_cast<const uint32_t(*)[16]>(&o[0]));
+                            tc::tmem_store16(ot + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&o[16]));
                         }
                     }
                 }

@@ -36,7 +36,7 @@ __device__ __forceinline__ int request_of(const BatchView& bt, int token) {
     int lo = 0, hi = bt.batch;  // q_start[lo] <= token < q_start[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (bt.q_start[mid] <= token) lo = mid;
+        if (load_word(bt.q_start + mid) <= token) lo = mid;
         else hi = mid;
     }
     return lo;

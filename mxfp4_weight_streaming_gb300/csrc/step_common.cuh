@@ -47,24 +47,33 @@ struct BatchView {
     int tokens;
 };
 
-// Plain loads here and below: a kernel may be resident before the one that
-// writes these arrays has ended (programmatic dependent launch), which the
-// read-only path does not allow for.
+// A word of an array that an earlier kernel of the stream may have written: a
+// kernel can be resident before that one has ended (programmatic dependent
+// launch), which the read-only path does not allow for. Volatile: never ahead
+// of pdl_wait_previous(); without a memory clobber, so that several are under
+// way at once (loads kept in order with shared stores made a call 6 us longer).
+__device__ __forceinline__ int load_word(const int* p) {
+    int v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 // Request b's rows of q [first, first + n) and its cache length, clamped to
 // what the arrays and the table can hold, so a wrong length on the device
 // never leads outside a buffer.
 __device__ __forceinline__ void request_extent(const BatchView& bt, int b, int& first, int& n, int& seq) {
-    const int lo = min(max(bt.q_start[b], 0), bt.tokens);
-    const int hi = min(max(bt.q_start[b + 1], lo), bt.tokens);
+    const int a = load_word(bt.q_start + b), z = load_word(bt.q_start + b + 1), len = load_word(bt.seq_lens + b);
+    const int lo = min(max(a, 0), bt.tokens);
+    const int hi = min(max(z, lo), bt.tokens);
     first = lo;
     n = hi - lo;
-    seq = min(max(bt.seq_lens[b], 0), bt.room);
+    seq = min(max(len, 0), bt.room);
 }
 
 // Page of cache index `at` (< table_width << page_shift), or -1 when the
 // table's entry lies outside the pool.
 __device__ __forceinline__ int page_of(const BatchView& bt, int b, int at, int page_shift, int num_pages) {
-    const int p = bt.block_table[b * bt.table_stride + (at >> page_shift)];
+    const int p = load_word(bt.block_table + b * bt.table_stride + (at >> page_shift));
     return (p >= 0 && p < num_pages) ? p : -1;
 }
 
