@@ -245,3 +245,48 @@ def test_a_wait_that_runs_out_is_reported(dtype, news, heads, cap):
     assert mx.last_device_status() == mx.MXFP4_OK
     ref, _, mag = attention_ref(pg, q, 0.1, cap)
     check(out, ref, attention_bound(ref, mag, dtype), "after the timeout")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page,dim", [(16, 128), (32, 64), (64, 128), (128, 64), (256, 128), (1024, 64)])
+def test_page_sizes_with_many_rows(page, dim, dtype):
+    """Pages smaller and larger than the 128-key tiles, K and V interleaved in one pool, nonsense in unused entries."""
+    lens = [2 * page + 45, 47, page - 1 if page > 64 else 5 * page]
+    pg = Paged(page + dim, lens, 2, dim, page, dtype, interleave=True, junk=-7)
+    run(pg, [45, 47, 9], 8, strided=True, what=f"many rows, page {page}")
+    run(pg, [45, 47, 9], 30, what=f"two row tiles, page {page}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("news,heads", [([3, 1], 4), ([30, 2], 4), ([150, 7], 4)])
+def test_negative_and_zero_scale(news, heads, dtype):
+    for scale, cap in ((-0.1, 0.0), (-0.2, 5.0), (0.0, 0.0)):
+        pg = Paged(news[0], [400, 77], 2, 64, 16, dtype)
+        run(pg, news, heads, scale=scale, softcap=cap, what=f"scale {scale} cap {cap}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_many_requests_with_many_rows(dtype):
+    """More requests than the kernel counts one by one, of different lengths, some without new tokens."""
+    news = [(i * 7) % 11 for i in range(130)]
+    lens = [n + (i * 53) % 300 for i, n in enumerate(news)]
+    run(Paged(21, lens, 1, 64, 16, dtype), news, 8, what="130 requests of up to 80 rows")
+
+
+def test_far_pages_with_many_rows():
+    page, kv, dim = 64, 8, 128
+    pages = (1 << 32) // (page * kv * dim) + 9
+    kp = torch.empty(pages, kv, page, dim, dtype=BF16, device="cuda")
+    vp = torch.empty(pages, kv, page, dim, dtype=BF16, device="cuda")
+    pg = Paged(12, [190], kv, dim, page, spare=0)
+    order = torch.arange(pages - 3, pages, device="cuda")
+    kp[order], vp[order] = pg.kp[pg.table[0].long()], pg.vp[pg.table[0].long()]
+    pg.kp, pg.vp, pg.table = kp, vp, order.to(torch.int32)[None].contiguous()
+    run(pg, [40], 16, what="far pages, many rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("heads", [97, 128])
+def test_widest_groups(heads, dtype):
+    pg = Paged(heads, [300, 20], 1, 64, 16, dtype)
+    run(pg, [2, 5], heads, what=f"group of {heads}")
