@@ -10,6 +10,10 @@
 // and r and y written once, and the next row's loads are in flight meanwhile.
 // Everything is fp32 until the one rounding of each output; y is the norm of
 // the unrounded r.
+//
+// Bound by HBM: 4,096 tokens of 7,168 with a gate per token, 294 MB, take 51
+// us, 84 % of the copy rate (82 us with a block per row and no loads ahead);
+// 4 tokens take 3.1 us, a launch.
 #include "step_launch.h"
 
 #include "step_common.cuh"
