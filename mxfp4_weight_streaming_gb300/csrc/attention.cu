@@ -700,13 +700,13 @@ cudaError_t launch_attention(const AttentionArgs& a, const CacheView& cache, con
         p.negate = a.scale < 0.f;
         // Masked scores are -inf and are multiplied by `mul`: it may not be 0.
         p.map = attn::score_map(fmaxf(fabsf(a.scale), 1e-36f), a.softcap);
-        return attn::launch_tc(p, a.e4m3, rows, num_sms, stream);
+        return attn::launch_tc(p, a.e4m3, rows, a.max_seq, num_sms, stream);
     }
     p.map = attn::score_map(a.scale, a.softcap);
     const int mt = rows <= 16 ? 1 : 2;
     p.cut.row_shift = mt == 1 ? 4 : 5;
     p.cut.key_shift = attn::kKeyShift;
-    const int ctas = attn::ctas_per_sm(cache.head_dim, a.e4m3, mt) * num_sms;
+    const int ctas = attn::ctas_for(p, rows, a.max_seq, attn::ctas_per_sm(cache.head_dim, a.e4m3, mt) * num_sms);
     return cache.head_dim == 64 ? attn::launch_d<64>(p, a.e4m3, mt, ctas, stream)
                                 : attn::launch_d<128>(p, a.e4m3, mt, ctas, stream);
 }

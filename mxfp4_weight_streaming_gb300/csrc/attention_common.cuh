@@ -233,9 +233,19 @@ struct Params {
 // Joins the parts that `ctas` CTAs left in the workspace (attention.cu).
 cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cudaStream_t stream);
 
+// CTAs for a call: no more than it has key tiles if the caller's bounds hold
+// (and no less work is done if they do not: each CTA's run is longer then). A
+// token over 1,000 has 128 tiles for 304 CTAs.
+inline int ctas_for(const Params& p, int64_t max_rows, int max_seq, int most) {
+    const int64_t rows = (max_rows + (1 << p.cut.row_shift) - 1) >> p.cut.row_shift;
+    const int64_t keys = (static_cast<int64_t>(max_seq) >> p.cut.key_shift) + 2;
+    const int64_t tiles = rows * keys * p.cut.kv_heads * p.batch.batch;
+    return tiles < most ? static_cast<int>(tiles) : most;
+}
+
 // The tensor-core kernel (attention_tc.cu): any number of rows.
 size_t tc_workspace_bytes(int64_t rows, int d, int num_sms);
-cudaError_t launch_tc(const Params& p, bool e4m3, int64_t rows, int num_sms, cudaStream_t stream);
+cudaError_t launch_tc(const Params& p, bool e4m3, int64_t rows, int max_seq, int num_sms, cudaStream_t stream);
 
 inline ScoreMap score_map(float scale, float softcap) {
     ScoreMap m;

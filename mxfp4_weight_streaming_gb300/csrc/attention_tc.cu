@@ -1077,7 +1077,7 @@ size_t tc_workspace_bytes(int64_t rows, int d, int num_sms) {
     return parts_bytes(num_sms, is_split(rows) ? 128 : 256, d);
 }
 
-cudaError_t launch_tc(const Params& in, bool e4m3, int64_t rows, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tc(const Params& in, bool e4m3, int64_t rows, int max_seq, int num_sms, cudaStream_t stream) {
     Params p = in;
     const bool split = is_split(rows);
     p.cut.row_shift = split ? 7 : 8;
@@ -1088,13 +1088,14 @@ cudaError_t launch_tc(const Params& in, bool e4m3, int64_t rows, int num_sms, cu
     if (e == cudaSuccess) e = pool_maps(dev, p.cache, e4m3, &maps);
     if (e != cudaSuccess) return e;
     const CUtensorMap &k = maps->k, &v = maps->v;
+    const int ctas = ctas_for(p, rows, max_seq, num_sms);
     if (p.cache.head_dim == 64)
-        e = e4m3 ? launch_d<64, true>(p, split, k, v, num_sms, stream)
-                 : launch_d<64, false>(p, split, k, v, num_sms, stream);
+        e = e4m3 ? launch_d<64, true>(p, split, k, v, ctas, stream)
+                 : launch_d<64, false>(p, split, k, v, ctas, stream);
     else
-        e = e4m3 ? launch_d<128, true>(p, split, k, v, num_sms, stream)
-                 : launch_d<128, false>(p, split, k, v, num_sms, stream);
-    return e == cudaSuccess ? launch_join(p, e4m3, true, num_sms, stream) : e;
+        e = e4m3 ? launch_d<128, true>(p, split, k, v, ctas, stream)
+                 : launch_d<128, false>(p, split, k, v, ctas, stream);
+    return e == cudaSuccess ? launch_join(p, e4m3, true, ctas, stream) : e;
 }
 
 }  // namespace attn
