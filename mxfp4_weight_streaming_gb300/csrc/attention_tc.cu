@@ -653,15 +653,28 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             // Once the last segment's products have read theirs.
             ok = __all_sync(0xffffffffu, turn < 2 || mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
             if (!ok) break;
+            // A lane copies one 16-byte chunk of every S-th row; the row's place
+            // in q (head of the group, then the next token) moves along with it.
+            constexpr int S = 32 / (D / 8);
+            const int c = lane % (D / 8), r0 = lane / (D / 8);
+            const int tok = cut.by_group.div(g.row0 + r0);
+            int h = g.row0 + r0 - tok * cut.group;
+            const __nv_bfloat16* src = p.q + (g.q0 + tok) * p.q_stride + (g.head * cut.group + h) * D + 8 * c;
+            const int64_t wrap = p.q_stride - static_cast<int64_t>(cut.group) * D;
+            const uint32_t to = base + (c >> 3) * L::kHalf;
 #pragma unroll 4
-            for (int i = lane; i < R * (D / 8); i += 32) {
-                const int r = i / (D / 8), c = i % (D / 8);
-                const __nv_bfloat16* src = q_row(p, g, r);
-                const uint32_t dst =
-                    base + (r >> 7) * L::kTile + (c >> 3) * L::kHalf + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                             "l"(src ? src + 8 * c : p.q), "r"(src ? 16 : 0)
+            for (int r = r0; r < R; r += S) {
+                const uint32_t dst = to + (r >> 7) * L::kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+                const bool in = r < g.rows;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? src : p.q),
+                             "r"(in ? 16 : 0)
                              : "memory");
+                src += S * D;
+                h += S;
+                for (int k = 0; k < S && h >= cut.group; ++k) {
+                    h -= cut.group;
+                    src += wrap;
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_shared();
