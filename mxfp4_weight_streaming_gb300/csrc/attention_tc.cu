@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             mbar_init(smem_addr(&sh.raw_empty[i]), 128);
         }
         mbar_init(smem_addr(&sh.patch), 1);
-        mbar_init(smem_addr(&sh.q_full), E4M3 ? 128 : 32);
+        mbar_init(smem_addr(&sh.q_full), E4M3 ? 128 : 288);
         mbar_init(smem_addr(&sh.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&sh.s_full[s]), 1);
@@ -650,8 +650,14 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
         bool ok = true;
         Segment g;
         while (ok && take_segment(sh, turn, g, wait)) {
-            // Once the last segment's products have read theirs.
-            ok = __all_sync(0xffffffffu, turn < 2 || mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
+            // The first segment's rows come from the softmax warps, idle then (one
+            // warp takes 10,000 cycles over 256 rows); later ones while those are
+            // at work, once the last segment's products have read theirs.
+            if (turn == 1) {
+                mbar_arrive(smem_addr(&sh.q_full));
+                continue;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
             if (!ok) break;
             // A lane copies one 16-byte chunk of every S-th row; the row's place
             // in q (head of the group, then the next token) moves along with it.
@@ -678,7 +684,10 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_shared();
-            mbar_arrive(smem_addr(&sh.q_full));
+            // 9 arrivals a lane stand for the 288 of the first segment.
+            asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], 9;\n\t}" ::"r"(
+                             smem_addr(&sh.q_full))
+                         : "memory");
         }
     } else if (warp >= kConvertWarp) {
         uint32_t turn = 0, count = 0;
@@ -782,6 +791,21 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
         };
 
         while (ok && take_segment(sh, turn_seg, g, wait)) {
+            if (!E4M3 && turn_seg == 1) {
+#pragma unroll 4
+                for (int i = threadIdx.x; i < R * (D / 8); i += 256) {
+                    const int row = i / (D / 8), c = i % (D / 8);
+                    const __nv_bfloat16* src = q_row(p, g, row);
+                    const uint32_t dst = base + (row >> 7) * L::kTile + (c >> 3) * L::kHalf + (row & 127) * 128 +
+                                         (((c & 7) ^ (row & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                                 "l"(src ? src + 8 * c : p.q), "r"(src ? 16 : 0)
+                                 : "memory");
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_shared();
+                mbar_arrive(smem_addr(&sh.q_full));
+            }
             const int tr = (SPLIT ? 0 : wg * 128) + r;  // row in the row tile
             const bool in = tr < g.rows;
             const int tok = cut.by_group.div(g.row0 + (in ? tr : 0)), pos = g.start + tok;
