@@ -81,7 +81,7 @@ struct alignas(16) Segment {
 template <bool SPLIT, bool E4M3>
 struct Shared {
     int64_t before[kGroups + 1];
-    uint64_t kv_full[8], kv_empty[8], raw_full[8], raw_empty[8], patch, q_full, q_empty, s_full[2], p_full[2][2],
+    uint64_t kv_full[8], kv_empty[8], raw_full[8], raw_empty[8], patch, q_full[2], q_empty, s_full[2], p_full[2][2],
         pv_done[2], vote[2], meet, drain, seg_full[2], seg_empty[2];
     Segment seg[2];
     float m[2][SPLIT ? 128 : 1], l[2][SPLIT ? 128 : 1];  // of the two streams' rows
@@ -442,9 +442,9 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             mbar_init(smem_addr(&sh.raw_empty[i]), 128);
         }
         mbar_init(smem_addr(&sh.patch), 1);
-        mbar_init(smem_addr(&sh.q_full), E4M3 ? 128 : 288);
         mbar_init(smem_addr(&sh.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&sh.q_full[s]), E4M3 ? 128 : 288);
             mbar_init(smem_addr(&sh.s_full[s]), 1);
             mbar_init(smem_addr(&sh.p_full[s][0]), 128);
             mbar_init(smem_addr(&sh.p_full[s][1]), 128);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
         };
         while (ok && take_segment(sh, turn, g, wait)) {
             const int n = __shfl_sync(0xffffffffu, g.steps, 0);
-            if (!wait_for(sh.q_full, (turn - 1) & 1)) break;
+            if (!wait_for(sh.q_full[(turn - 1) & 1], ((turn - 1) >> 1) & 1)) break;
             if constexpr (SPLIT) {
                 // Ring order: K0 K1 V0 K2 V1 K3 ...
                 auto k_at = [&](int j) { return used + k_place<SPLIT>(j); };
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             // warp takes 10,000 cycles over 256 rows); later ones while those are
             // at work, once the last segment's products have read theirs.
             if (turn == 1) {
-                mbar_arrive(smem_addr(&sh.q_full));
+                mbar_arrive(smem_addr(&sh.q_full[0]));
                 continue;
             }
             ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             fence_proxy_async_shared();
             // 9 arrivals a lane stand for the 288 of the first segment.
             asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], 9;\n\t}" ::"r"(
-                             smem_addr(&sh.q_full))
+                             smem_addr(&sh.q_full[(turn - 1) & 1]))
                          : "memory");
         }
     } else if (warp >= kConvertWarp) {
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
                 sh.q_exp[(turn - 1) & 1][r] = static_cast<int8_t>(e);
             }
             fence_proxy_async_shared();
-            mbar_arrive(smem_addr(&sh.q_full));
+            mbar_arrive(smem_addr(&sh.q_full[(turn - 1) & 1]));
         };
         while (ok && take_segment(sh, turn, g, wait)) {
 #pragma unroll 1
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_shared();
-                mbar_arrive(smem_addr(&sh.q_full));
+                mbar_arrive(smem_addr(&sh.q_full[0]));
             }
             const int tr = (SPLIT ? 0 : wg * 128) + r;  // row in the row tile
             const bool in = tr < g.rows;
@@ -816,15 +816,20 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             // This row's first and last visible key.
             const int first = max(g.begin, cut.window ? pos - cut.window + 1 : 0);
             const int last = in ? min(cut.tree ? g.end - 1 : pos, g.end - 1) : -1;
+            const int n_all = g.steps, n_my = SPLIT ? (n_all + 1 - wg) / 2 : n_all;
             float mul = p.map.mul;
-            if constexpr (E4M3) {
-                if (!wait_all(sh.q_full, (turn_seg - 1) & 1)) break;
+            // q_full alternates between two barriers: q of the segment after next
+            // waits for this one's last probabilities, so no group with tiles can
+            // still be here when its barrier's phase comes round again (on one
+            // barrier the next segment's q would do that, from the moment this
+            // one's last scores are taken). A group without tiles has no use for it.
+            if (E4M3 && n_my) {
+                if (!wait_all(sh.q_full[(turn_seg - 1) & 1], ((turn_seg - 1) >> 1) & 1)) break;
                 const int e = sh.q_exp[(turn_seg - 1) & 1][(SPLIT ? 0 : wg * 128) + r];
                 const float ks = p.cache.k_scale ? p.cache.k_scale[g.head] : 1.f;
                 mul = fmaxf(mul * ks * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 1e-36f);
             }
             float m = -INFINITY, l = 0.f;
-            const int n_all = g.steps, n_my = SPLIT ? (n_all + 1 - wg) / 2 : n_all;
 
             for (int jj = 0; jj < n_my; ++jj) {
                 const int j = SPLIT ? 2 * jj + wg : jj;
