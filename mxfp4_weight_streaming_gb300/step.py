@@ -72,6 +72,18 @@ def _ints(t, count, name):
         raise ValueError(f"{name}: contiguous int32 CUDA tensor of {count} expected, got {t.dtype} {list(t.shape)}")
 
 
+def _row_stride(table):
+    """Entries between a block table's rows. A row that several requests
+    share by expand() has a stride of 0, which the C side takes as dense."""
+    rows, width = table.shape
+    if rows < 2:
+        return width
+    stride = table.stride(0)
+    if stride < width:
+        raise ValueError("block_table: rows of their own expected, not an expanded tensor")
+    return stride
+
+
 def _stream_of(stream, *made):
     """The raw handle of a stream given by the caller. Tensors made for the
     call are kept until that stream's work on them is done."""
@@ -96,6 +108,9 @@ class KVCache:
               "k and v: bf16 or float8_e4m3fn CUDA tensors expected")
         pages, heads, page, dim = k.shape[-4:]
         _need(k.stride(-1) == 1 and k.stride(-2) == dim and k.stride(-3) == page * dim, "a page has to be dense")
+        # A stride of 0 (an expanded tensor) would mean "dense" to the C side.
+        for d in range(k.dim() - 3):
+            _need(k.shape[d] == 1 or k.stride(d) >= heads * page * dim, "pages and layers may not share memory")
         e4m3 = k.dtype == torch.float8_e4m3fn
         for sc in (k_scale, v_scale):
             _need(sc is None or (e4m3 and sc.is_cuda and sc.dtype == torch.float32 and sc.shape == (heads,)
@@ -130,7 +145,7 @@ class KVBatch:
         self.q_start, self.seq_lens, self.block_table = q_start, seq_lens, block_table
         self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), int(max_q), int(max_seq)
         width = block_table.shape[1]
-        stride = block_table.stride(0) if b > 1 else width
+        stride = _row_stride(block_table)
         self.struct = KVBatchStruct(_ptr(q_start), _ptr(seq_lens), _ptr(block_table), stride, width, b, self.tokens,
                                     self.max_q, self.max_seq, 0)
         self.ref = ctypes.addressof(self.struct)
@@ -300,7 +315,7 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.shape[0] != old or \
             block_table.stride(1) != 1 or not block_table.is_cuda:
         raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
-    width = block_table.shape[1]
+    width, stride = block_table.shape[1], _row_stride(block_table)
     # Four allocations take 6 us of host time, one that is split and viewed 12.
     dev = block_table.device
     table = _empty((n, width), dtype=_I32, device=dev)
@@ -310,7 +325,7 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     ws = cache_workspace(n, cache.num_pages, dev) if workspace is None else workspace
     raw = _raw_stream(table.get_device()) if stream is None else _stream_of(stream, table, lens, copies, info, ws)
     rc = (_L or _lib()).mxfp4_cache_update(
-        block_table.data_ptr(), block_table.stride(0) if old > 1 else width, width, seq_lens.data_ptr(), old,
+        block_table.data_ptr(), stride, width, seq_lens.data_ptr(), old,
         parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, table.data_ptr(),
         lens.data_ptr(), copies.data_ptr(), info.data_ptr(), ws.data_ptr(), ws.nbytes, raw)
     if rc:
