@@ -6,7 +6,8 @@ definitions). Argument marshalling only, as in the rest of the binding.
 `KVCache` and `KVBatch` hold tensors and the C structs that point into them;
 a program makes them once and passes them to every call. Their tensors are
 read on the device by each call, so their contents (lengths, page numbers)
-may change between calls, their addresses may not.
+may change between calls, their addresses may not. All tensors of a call lie
+on the current GPU.
 """
 from __future__ import annotations
 
@@ -50,6 +51,18 @@ def _lib():
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_device(device, *tensors):
+    """Every tensor of a call (or None) on the GPU that the library's launch goes to, the current one."""
+    if device != _current_device():
+        raise ValueError(f"tensors on GPU {device}, but the current one is {_current_device()}")
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor on device {t.get_device()} (-1: the host) among tensors of GPU {device}")
 
 
 def _fail(rc: int, what: str):
@@ -115,6 +128,8 @@ class KVCache:
         for sc in (k_scale, v_scale):
             _need(sc is None or (e4m3 and sc.is_cuda and sc.dtype == torch.float32 and sc.shape == (heads,)
                                  and sc.is_contiguous()), "scales: float32 [kv_heads] of an E4M3 cache expected")
+        for t in (v, k_scale, v_scale):
+            _need(t is None or t.get_device() == k.get_device(), "pools and scales: tensors of one GPU expected")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.layers = k.shape[0] if k.dim() == 5 else 1
@@ -142,6 +157,8 @@ class KVBatch:
         _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2
               and block_table.shape[0] == b and block_table.stride(1) == 1,
               "block_table: int32 CUDA tensor [batch, width] expected")
+        _need(seq_lens.get_device() == q_start.get_device() == block_table.get_device(),
+              "q_start, seq_lens and block_table: tensors of one GPU expected")
         self.q_start, self.seq_lens, self.block_table = q_start, seq_lens, block_table
         self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), int(max_q), int(max_seq)
         width = block_table.shape[1]
@@ -175,9 +192,11 @@ def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=No
             raise ValueError("outputs: contiguous bf16 [tokens, n] expected")
     if kind != "rms" and kind != "layer":
         raise ValueError("kind: 'rms' or 'layer' expected")
+    device = x.get_device()
+    _on_device(device, residual, weight, post_weight, post_bias, gate, bias, out, residual_out)
     y = torch.empty_like(x) if out is None else out
     r = torch.empty_like(x) if residual_out is None else residual_out
-    raw = _raw_stream(x.get_device()) if stream is None else _stream_of(stream, y, r)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, y, r)
     rc = (_L or _lib()).mxfp4_residual_norm(
         x.data_ptr(), residual.data_ptr(), t, n, None if post_weight is None else post_weight.data_ptr(),
         _ptr(post_bias), _ptr(gate), gate_stride, scale, weight.data_ptr(), _ptr(bias), weight_offset, eps,
@@ -241,13 +260,15 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
         rotary = 2 * inv_freq.numel()
     if positions is not None:
         _ints(positions, tokens, "positions")
+    device = qkv.get_device()
+    _on_device(device, cache.k, batch.q_start, inv_freq, positions, out)
     if out is None:
         q = _empty((tokens, q_heads, d), dtype=_BF16, device=qkv.device)
     else:
         _need(out.dtype is _BF16 and out.shape == (tokens, q_heads, d) and out.is_contiguous(),
               "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
         q = out
-    raw = _raw_stream(qkv.get_device()) if stream is None else _stream_of(stream, q)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, q)
     rc = (_L or _lib()).mxfp4_rope_append(
         qkv.data_ptr(), qkv.stride(0), q_heads, _ptr(positions), _ptr(inv_freq), rotary, interleaved, factor,
         cache.ref, batch.ref, q.data_ptr(), raw)
@@ -275,6 +296,8 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
     if tree_mask is not None:
         _need(tree_mask.dtype is _I64 and tree_mask.shape == (tokens,) and tree_mask.is_contiguous(),
               "tree_mask: int64 [tokens] expected")
+    device = q.get_device()
+    _on_device(device, cache.k, batch.q_start, tree_mask, out, lse, workspace)
     if out is None:
         o = _empty(shape, dtype=_BF16, device=q.device)
     else:
@@ -285,7 +308,7 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
         _need(lse.dtype is _F32 and lse.shape == shape[:2] and lse.is_contiguous(),
               "lse: contiguous float32 [tokens, q_heads] expected")
     ws = attention_workspace(heads, cache, batch) if workspace is None else workspace
-    raw = _raw_stream(q.get_device()) if stream is None else _stream_of(stream, o, ws)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, o, ws)
     rc = (_L or _lib()).mxfp4_attention(
         q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
         d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), o.data_ptr(), _ptr(lse),
@@ -315,6 +338,8 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.shape[0] != old or \
             block_table.stride(1) != 1 or not block_table.is_cuda:
         raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
+    device = block_table.get_device()
+    _on_device(device, seq_lens, parent, keep, grow, workspace)
     width, stride = block_table.shape[1], _row_stride(block_table)
     # Four allocations take 6 us of host time, one that is split and viewed 12.
     dev = block_table.device
@@ -323,7 +348,7 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     copies = _empty((n, 3), dtype=_I32, device=dev)
     info = _empty(2, dtype=_I32, device=dev)
     ws = cache_workspace(n, cache.num_pages, dev) if workspace is None else workspace
-    raw = _raw_stream(table.get_device()) if stream is None else _stream_of(stream, table, lens, copies, info, ws)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, table, lens, copies, info, ws)
     rc = (_L or _lib()).mxfp4_cache_update(
         block_table.data_ptr(), stride, width, seq_lens.data_ptr(), old,
         parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, table.data_ptr(),
@@ -337,7 +362,9 @@ def cache_copy(cache, copies, stream=None):
     """Copies the page rows that cache_update lists, in every layer of the cache."""
     n = copies.shape[0]
     _ints(copies, 3 * n, "copies")
-    raw = _raw_stream(copies.get_device()) if stream is None else _stream_of(stream)
+    device = copies.get_device()
+    _on_device(device, cache.k)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream)
     rc = (_L or _lib()).mxfp4_cache_copy(cache.ref, copies.data_ptr(), n, raw)
     if rc:
         _fail(rc, "mxfp4_cache_copy")
@@ -350,12 +377,14 @@ def cache_accept(cache, batch, path, n_accept, out=None, stream=None):
     n, length = batch.batch, path.shape[1]
     _ints(path, n * length, "path")
     _ints(n_accept, n, "n_accept")
+    device = path.get_device()
+    _on_device(device, cache.k, batch.q_start, n_accept, out)
     if out is None:
         lens = _empty(n, dtype=_I32, device=path.device)
     else:
         _ints(out, n, "out")
         lens = out
-    raw = _raw_stream(path.get_device()) if stream is None else _stream_of(stream, lens)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, lens)
     rc = (_L or _lib()).mxfp4_cache_accept(cache.ref, batch.ref, path.data_ptr(), length, n_accept.data_ptr(),
                                            lens.data_ptr(), raw)
     if rc:

@@ -43,6 +43,7 @@ def library(monkeypatch):
     lib = Library()
     monkeypatch.setattr(step, "_L", lib)
     monkeypatch.setattr(step, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(step, "_current_device", lambda: 0, raising=False)
     return lib
 
 
@@ -88,3 +89,103 @@ def test_expanded_pools_are_refused(layers):
         mx.KVCache(*same)
     if layers is None:
         assert mx.KVCache(*[OnGpu(one) for _ in range(2)]).struct.page_stride == 2 * 16 * 64
+
+
+# ------------------------------------------------------------------- devices
+def bf16(*shape, device=0):
+    return OnGpu(torch.zeros(shape, dtype=BF16), device)
+
+
+def a_batch(device=0, width=4):
+    return mx.KVBatch(ints(3, device=device), ints(2, device=device), ints(2, width, device=device), tokens=4, max_q=2,
+                      max_seq=60)
+
+
+def norm_call(**kw):
+    a = dict(x=bf16(4, 64), residual=bf16(4, 64), weight=bf16(64), post_weight=bf16(64), post_bias=bf16(64),
+             gate=bf16(4, 64), bias=bf16(64), out=bf16(4, 64), residual_out=bf16(4, 64))
+    return mx.residual_norm, dict(a, **kw)
+
+
+def rope_call(**kw):
+    a = dict(qkv=bf16(4, 8 * 64), q_heads=4, inv_freq=OnGpu(torch.zeros(32)), cache=mx.KVCache(*pools()),
+             batch=a_batch(), positions=ints(4), out=bf16(4, 4, 64))
+    return mx.rope_append, dict(a, **kw)
+
+
+def attention_call(**kw):
+    a = dict(q=bf16(4, 4, 64), cache=mx.KVCache(*pools()), batch=a_batch(),
+             tree_mask=OnGpu(torch.zeros(4, dtype=torch.int64)), out=bf16(4, 4, 64), lse=OnGpu(torch.zeros(4, 4)),
+             workspace=OnGpu(torch.zeros(256, dtype=torch.uint8)))
+    return mx.attention, dict(a, **kw)
+
+
+def update_call(**kw):
+    a = dict(cache=mx.KVCache(*pools()), block_table=ints(2, 4), seq_lens=ints(2), parent=ints(3), keep=ints(3),
+             grow=ints(3), workspace=OnGpu(torch.zeros(256, dtype=torch.uint8)))
+    return mx.cache_update, dict(a, **kw)
+
+
+def copy_call(**kw):
+    return mx.cache_copy, dict(dict(cache=mx.KVCache(*pools()), copies=ints(2, 3)), **kw)
+
+
+def accept_call(**kw):
+    a = dict(cache=mx.KVCache(*pools()), batch=a_batch(), path=ints(2, 3), n_accept=ints(2), out=ints(2))
+    return mx.cache_accept, dict(a, **kw)
+
+
+CALLS = dict(norm=norm_call, rope=rope_call, attention=attention_call, update=update_call, copy=copy_call,
+             accept=accept_call)
+OPERANDS = [(name, key) for name, make in CALLS.items() for key, v in make()[1].items()
+            if isinstance(v, (OnGpu, mx.KVCache, mx.KVBatch))]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_one_gpu_go_through(name, library):
+    f, a = CALLS[name]()
+    f(**a)
+    assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("name,key", [x for x in OPERANDS if x != ("update", "cache")])
+@pytest.mark.parametrize("device", [-1, 1])
+def test_an_operand_elsewhere_is_refused(name, key, device, library):
+    """One tensor (or cache, or batch) on the host or on another GPU."""
+    f, a = CALLS[name]()
+    if key == "cache":
+        if device < 0:
+            return  # a cache on the host cannot be made
+        a[key] = mx.KVCache(*pools(device=device))
+    elif key == "batch":
+        if device < 0:
+            return
+        a[key] = a_batch(device=device)
+    else:
+        a[key] = OnGpu(a[key].t, device)
+    with pytest.raises(ValueError):
+        f(**a)
+    assert not library.calls
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_another_current_gpu_is_refused(name, library, monkeypatch):
+    f, a = CALLS[name]()
+    monkeypatch.setattr(step, "_current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        f(**a)
+    assert not library.calls
+
+
+def test_handles_over_two_devices_are_refused():
+    k, v = pools()
+    with pytest.raises(ValueError):
+        mx.KVCache(k, OnGpu(v.t, 1))
+    e = [OnGpu(p.t.to(torch.float8_e4m3fn)) for p in (k, v)]
+    with pytest.raises(ValueError):
+        mx.KVCache(*e, k_scale=OnGpu(torch.ones(2), 1))
+    for bad in range(3):
+        args = [ints(3), ints(2), ints(2, 4)]
+        args[bad] = OnGpu(args[bad].t, 1)
+        with pytest.raises(ValueError):
+            mx.KVBatch(*args, tokens=4, max_q=2, max_seq=60)
