@@ -56,13 +56,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _elsewhere():
+    raise ValueError("every tensor of a call has to be on one GPU, the current one; one is on the host or on another GPU")
+
+
 def _on_device(device, *tensors):
-    """Every tensor of a call (or None) on the GPU that the library's launch goes to, the current one."""
+    """Each of these (or None) on `device`, which has to be the current GPU: the library's launch goes there."""
     if device != _current_device():
-        raise ValueError(f"tensors on GPU {device}, but the current one is {_current_device()}")
+        _elsewhere()
     for t in tensors:
         if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor on device {t.get_device()} (-1: the host) among tensors of GPU {device}")
+            _elsewhere()
 
 
 def _fail(rc: int, what: str):
@@ -79,10 +83,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ints(t, count, name):
+def _ints(t, count, name, device):
     """An int32 vector or matrix the C side can take as it lies in memory."""
-    if t.dtype is not _I32 or t.numel() != count or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not _I32 or t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 CUDA tensor of {count} expected, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != device:
+        _elsewhere()
 
 
 def _row_stride(table):
@@ -128,8 +134,9 @@ class KVCache:
         for sc in (k_scale, v_scale):
             _need(sc is None or (e4m3 and sc.is_cuda and sc.dtype == torch.float32 and sc.shape == (heads,)
                                  and sc.is_contiguous()), "scales: float32 [kv_heads] of an E4M3 cache expected")
+        self.device = k.get_device()
         for t in (v, k_scale, v_scale):
-            _need(t is None or t.get_device() == k.get_device(), "pools and scales: tensors of one GPU expected")
+            _need(t is None or t.get_device() == self.device, "pools and scales: tensors of one GPU expected")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.layers = k.shape[0] if k.dim() == 5 else 1
@@ -152,13 +159,12 @@ class KVBatch:
 
     def __init__(self, q_start, seq_lens, block_table, tokens, max_q, max_seq):
         b = seq_lens.numel()
-        _ints(seq_lens, b, "seq_lens")
-        _ints(q_start, b + 1, "q_start")
+        self.device = device = block_table.get_device()
+        _ints(seq_lens, b, "seq_lens", device)
+        _ints(q_start, b + 1, "q_start", device)
         _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2
               and block_table.shape[0] == b and block_table.stride(1) == 1,
               "block_table: int32 CUDA tensor [batch, width] expected")
-        _need(seq_lens.get_device() == q_start.get_device() == block_table.get_device(),
-              "q_start, seq_lens and block_table: tensors of one GPU expected")
         self.q_start, self.seq_lens, self.block_table = q_start, seq_lens, block_table
         self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), int(max_q), int(max_seq)
         width = block_table.shape[1]
@@ -253,15 +259,17 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
     if qkv.dtype is not _BF16 or qkv.shape != (tokens, (q_heads + 2 * cache.kv_heads) * d) or not qkv.is_cuda or \
             qkv.stride(1) != 1:
         raise ValueError("qkv: bf16 CUDA tensor [tokens, (q_heads + 2 kv_heads) * head_dim] expected")
+    device = qkv.get_device()
+    if cache.device != device or batch.device != device:
+        _elsewhere()
     rotary = 0
     if inv_freq is not None:
-        if inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
+        if inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq: float32 CUDA tensor [rotary_dim / 2] expected")
         rotary = 2 * inv_freq.numel()
     if positions is not None:
-        _ints(positions, tokens, "positions")
-    device = qkv.get_device()
-    _on_device(device, cache.k, batch.q_start, inv_freq, positions, out)
+        _ints(positions, tokens, "positions", device)
+    _on_device(device, inv_freq, out)
     if out is None:
         q = _empty((tokens, q_heads, d), dtype=_BF16, device=qkv.device)
     else:
@@ -297,7 +305,9 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
         _need(tree_mask.dtype is _I64 and tree_mask.shape == (tokens,) and tree_mask.is_contiguous(),
               "tree_mask: int64 [tokens] expected")
     device = q.get_device()
-    _on_device(device, cache.k, batch.q_start, tree_mask, out, lse, workspace)
+    if cache.device != device or batch.device != device:
+        _elsewhere()
+    _on_device(device, tree_mask, out, lse, workspace)
     if out is None:
         o = _empty(shape, dtype=_BF16, device=q.device)
     else:
@@ -329,17 +339,16 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     all), with room for grow[i] more. Returns (block_table, seq_lens, copies,
     info): int32 [n, width], [n], [n, 3] for cache_copy, and [pages left
     free, pages asked for in vain]."""
-    n, old = parent.numel(), seq_lens.numel()
-    _ints(parent, n, "parent")
-    _ints(grow, n, "grow")
-    _ints(seq_lens, old, "seq_lens")
+    n, old, device = parent.numel(), seq_lens.numel(), block_table.get_device()
+    _ints(parent, n, "parent", device)
+    _ints(grow, n, "grow", device)
+    _ints(seq_lens, old, "seq_lens", device)
     if keep is not None:
-        _ints(keep, n, "keep")
+        _ints(keep, n, "keep", device)
     if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.shape[0] != old or \
             block_table.stride(1) != 1 or not block_table.is_cuda:
         raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
-    device = block_table.get_device()
-    _on_device(device, seq_lens, parent, keep, grow, workspace)
+    _on_device(device, workspace)
     width, stride = block_table.shape[1], _row_stride(block_table)
     # Four allocations take 6 us of host time, one that is split and viewed 12.
     dev = block_table.device
@@ -360,10 +369,9 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
 
 def cache_copy(cache, copies, stream=None):
     """Copies the page rows that cache_update lists, in every layer of the cache."""
-    n = copies.shape[0]
-    _ints(copies, 3 * n, "copies")
-    device = copies.get_device()
-    _on_device(device, cache.k)
+    n, device = copies.shape[0], cache.device
+    _ints(copies, 3 * n, "copies", device)
+    _on_device(device)
     raw = _raw_stream(device) if stream is None else _stream_of(stream)
     rc = (_L or _lib()).mxfp4_cache_copy(cache.ref, copies.data_ptr(), n, raw)
     if rc:
@@ -374,15 +382,16 @@ def cache_accept(cache, batch, path, n_accept, out=None, stream=None):
     """Moves the rows of the accepted path (int32 [batch, path_len], indices
     among a request's new tokens; n_accept int32 [batch]) to the front of its
     new tokens, in every layer. Returns the lengths with the accepted tokens, int32 [batch]."""
-    n, length = batch.batch, path.shape[1]
-    _ints(path, n * length, "path")
-    _ints(n_accept, n, "n_accept")
-    device = path.get_device()
-    _on_device(device, cache.k, batch.q_start, n_accept, out)
+    n, length, device = batch.batch, path.shape[1], cache.device
+    _ints(path, n * length, "path", device)
+    _ints(n_accept, n, "n_accept", device)
+    if batch.device != device:
+        _elsewhere()
+    _on_device(device)
     if out is None:
         lens = _empty(n, dtype=_I32, device=path.device)
     else:
-        _ints(out, n, "out")
+        _ints(out, n, "out", device)
         lens = out
     raw = _raw_stream(device) if stream is None else _stream_of(stream, lens)
     rc = (_L or _lib()).mxfp4_cache_accept(cache.ref, batch.ref, path.data_ptr(), length, n_accept.data_ptr(),
