@@ -199,6 +199,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// The smaller one, NaN where either is (fminf gives the other).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Scores in the log2 domain: s * scale * log2(e), or with a cap
 // cap * tanh(s * scale / cap) * log2(e). tanh x = 1 - 2 / (1 + e^2x): off by
 // a few 1e-7 of the cap (the hardware's tanh, off by 5e-4 of it, would cost
@@ -208,7 +215,7 @@ struct ScoreMap {
     float cap;      // cap * log2(e); 0: no cap
     __device__ __forceinline__ float operator()(float s) const {
         if (cap == 0.f) return s * mul;
-        const float e = exp2_fast(fminf(s * mul, 80.f));
+        const float e = exp2_fast(min_nan(s * mul, 80.f));
         return cap - __fdividef(2.f * cap, 1.f + e);
     }
 };

@@ -1,9 +1,11 @@
 """mxfp4_attention where calls go to their limits."""
+import math
+
 import pytest
 import torch
 
 from gpu_cases import lib
-from step_cases import E4M3, Paged
+from step_cases import E4M3, Paged, attention_bound, attention_ref, check, gen, randn
 from test_attention_gpu import run
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +33,36 @@ def test_many_short_items_in_a_row(dim, kv, group, new, requests, dtype):
         again = mx.attention(q, cache, batch, workspace=ws)
         assert mx.last_device_status() == mx.MXFP4_OK
         assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+# ----------------------------------------------------- NaN and capped scores
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("news,heads", [([1], 8), ([5], 8), ([30], 8), ([70], 8)])
+def test_visible_nan_reaches_the_output(news, heads, cap, dtype):
+    """A NaN in a key that every query sees makes the outputs of its KV head
+    NaN, a NaN in q those of its own row; the rest stays right."""
+    mx = lib()
+    n, seq = news[0], news[0] + 90
+    pg = Paged(n + 50, [seq], 2, 64, 16, dtype)
+    q = randn(gen(n), n, heads, 64)
+    cache, batch = pg.cache(mx), pg.batch(mx, news)
+    ref, _, mag = attention_ref(pg, q, 0.125, cap)
+    bound = attention_bound(ref, mag, dtype)
+
+    bad = q.clone()
+    bad[n - 1, heads - 1, 5] = math.nan
+    out = mx.attention(bad, cache, batch, softcap=cap)
+    assert torch.isnan(out[n - 1, heads - 1].float()).all()
+    keep = torch.ones(n, heads, dtype=torch.bool, device="cuda")
+    keep[n - 1, heads - 1] = False
+    check(out[keep], ref[keep], bound[keep], "rows without the NaN")
+
+    p, r = int(pg.table[0, 40 // 16]), 40 % 16  # key 40, KV head 0
+    if dtype == E4M3:
+        pg.kp.view(torch.uint8)[p, 0, r, 3] = 0x7F
+    else:
+        pg.kp[p, 0, r, 3] = math.nan
+    out = mx.attention(q, cache, batch, softcap=cap)
+    assert torch.isnan(out[:, :heads // 2].float()).all()
+    check(out[:, heads // 2:], ref[:, heads // 2:], bound[:, heads // 2:], "the other KV head")
