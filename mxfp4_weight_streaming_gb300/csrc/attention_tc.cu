@@ -724,7 +724,9 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             mbar_arrive(smem_addr(&sh.kv_full[slot]));
             ++count;
         };
-        // q; 2^-e brings a row's largest magnitude to [1, 2).
+        // q; 2^-e brings a row's largest magnitude to [1, 2). The sign of its KV
+        // head's scale goes with it (or a NaN): the factor of the scores has to
+        // be positive, since masked ones are -inf.
         auto convert_q = [&]() {
             ok = ok && (turn < 2 || mbar_wait(smem_addr(&sh.q_empty), turn & 1, wait));
             if (!ok) return;
@@ -732,6 +734,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             for (int r = t; r < R; r += 128) {
                 const uint4* src = reinterpret_cast<const uint4*>(q_row(p, g, r));
                 const uint32_t row = base + (r >> 7) * L::kTile + (r & 127) * 128;
+                const float ks = p.cache.k_scale ? p.cache.k_scale[g.head] : 1.f;
                 float top = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
@@ -742,7 +745,8 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
                         top = fmaxf(top, fmaxf(fabsf(half_of<false>(u[x], 0)), fabsf(half_of<false>(u[x], 1))));
                 }
                 const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -120), 120);
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) *
+                                   (ks == ks ? copysignf(1.f, ks) : ks);
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     const uint4 w = src ? src[c] : make_uint4(0, 0, 0, 0);
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
                 const float ks = p.cache.k_scale ? p.cache.k_scale[g.head] : 1.f;
-                mul = fmaxf(mul * ks * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 1e-36f);
+                mul = fmaxf(fabsf(mul * ks * __uint_as_float(static_cast<uint32_t>(127 + e) << 23)), 1e-36f);
             }
             float m = -INFINITY, l = 0.f;
 

@@ -66,3 +66,33 @@ def test_visible_nan_reaches_the_output(news, heads, cap, dtype):
     out = mx.attention(q, cache, batch, softcap=cap)
     assert torch.isnan(out[:, :heads // 2].float()).all()
     check(out[:, heads // 2:], ref[:, heads // 2:], bound[:, heads // 2:], "the other KV head")
+
+
+# ------------------------------------------------------------ a head's scale
+@pytest.mark.parametrize("news,heads", [([3, 1], 4), ([30, 2], 4), ([150, 7], 4)])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("scale", [0.2, -0.2])
+def test_negative_and_zero_scales_of_a_head(news, heads, cap, scale):
+    """Element * scale of its KV head, whatever the scale's sign."""
+    pg = Paged(news[0] + 7, [400, 77], 3, 64, 16, E4M3)
+    for head, f in ((0, -1.0), (1, 0.0)):
+        pg.k_scale[head] *= f
+        pg.k = [k * torch.where(torch.arange(3, device="cuda") == head, f, 1.0)[:, None] for k in pg.k]
+    pg.v_scale[2] *= -1
+    pg.v = [v * torch.where(torch.arange(3, device="cuda") == 2, -1.0, 1.0)[:, None] for v in pg.v]
+    run(pg, news, heads * 3, scale=scale, softcap=cap, what=f"scales of heads, cap {cap}")
+
+
+@pytest.mark.parametrize("news", [[3], [40], [150]])
+def test_nan_scale_of_a_head(news):
+    """Its scores are NaN, and so is every row that sees a key; a row that sees none stays 0."""
+    mx = lib()
+    pg = Paged(5, [news[0] - 1], 2, 64, 16, E4M3)  # the first query lies before the sequence
+    pg.k_scale[1] = math.nan
+    q = randn(gen(3), news[0], 8, 64)
+    out = mx.attention(q, pg.cache(mx), pg.batch(mx, news))
+    pg.k_scale = pg.k_scale.nan_to_num(1.0)
+    pg.k = [k.nan_to_num(0.0) for k in pg.k]
+    ref, _, mag = attention_ref(pg, q, 0.125)
+    check(out[:, :4], ref[:, :4], attention_bound(ref, mag, E4M3)[:, :4], "the other KV head")
+    assert torch.isnan(out[1:, 4:].float()).all() and (out[0] == 0).all()
