@@ -224,7 +224,9 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
       "ramp"    frequencies that turn more than `fast` times over the trained
                 positions stay, those that turn less than `slow` times are
                 divided by factor, a linear ramp (over the pair's index)
-                between; q and k are scaled by 0.1 ln(factor) + 1.
+                between, whose slow end may lie past the last pair (up to
+                index rotary_dim - 1); q and k are scaled by 0.1 ln(factor) + 1
+                (Peng et al., 2023).
     """
     _need(rotary_dim >= 2 and rotary_dim % 2 == 0 and factor > 0, "rotary_dim: even, factor: positive expected")
     _need(scaling in (None, "linear", "base", "ramp"), "scaling: None, 'linear', 'base' or 'ramp' expected")
@@ -241,7 +243,7 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
         def pair_of(turns):  # the (fractional) pair that turns so often over the trained positions
             return rotary_dim * math.log(trained / (2 * math.pi * turns)) / (2 * math.log(base))
 
-        lo, hi = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), half - 1)
+        lo, hi = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), rotary_dim - 1)
         for j in range(half):
             stretched = min(max((j - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
             freq[j] *= 1.0 - stretched + stretched / factor

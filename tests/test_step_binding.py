@@ -189,3 +189,29 @@ def test_handles_over_two_devices_are_refused():
         args[bad] = OnGpu(args[bad].t, 1)
         with pytest.raises(ValueError):
             mx.KVBatch(*args, tokens=4, max_q=2, max_seq=60)
+
+
+# ------------------------------------------------------------- rotary ramp
+@pytest.mark.parametrize("dim,base,trained,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 4096, 8.0), (64, 1e4, 32768, 4.0),
+                                                     (128, 5e5, 8192, 16.0), (32, 1e4, 10 ** 6, 2.0)])
+def test_ramp_of_rope_frequencies(dim, base, trained, factor):
+    """A pair's share of the stretch by the turns it makes over the trained
+    positions, from the definition: none above 32, all below 1, linear in the
+    pair's index between the pairs that turn so often (whole indices around
+    them, the slow one at most rotary_dim - 1)."""
+    import math
+    freq, _ = mx.rope_frequencies(dim, base=base, scaling="ramp", factor=factor, trained=trained, device="cpu")
+
+    def index(turns):
+        return dim / 2 * math.log(trained / (turns * 2 * math.pi), base)
+
+    lo, hi = max(math.floor(index(32.0)), 0), min(math.ceil(index(1.0)), dim - 1)
+    for j in range(dim // 2):
+        plain = base ** (-2 * j / dim)
+        share = min(max((j - lo) / (hi - lo), 0.0), 1.0)
+        want = plain * ((1 - share) + share / factor)
+        assert abs(freq[j].item() - want) <= 1e-6 * want, j
+        if trained * plain / (2 * math.pi) > 32.0:
+            assert abs(freq[j].item() - plain) <= 1e-6 * plain
+        if trained * plain / (2 * math.pi) > 1.0:  # still turns: not stretched in full
+            assert freq[j].item() > plain / factor * (1 + 1e-6)
