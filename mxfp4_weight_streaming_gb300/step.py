@@ -7,7 +7,8 @@ definitions). Argument marshalling only, as in the rest of the binding.
 a program makes them once and passes them to every call. Their tensors are
 read on the device by each call, so their contents (lengths, page numbers)
 may change between calls, their addresses may not. All tensors of a call lie
-on the current GPU.
+on the current GPU. With stream= a call runs on that stream, and the results
+it makes are that stream's memory.
 """
 from __future__ import annotations
 
@@ -103,13 +104,26 @@ def _row_stride(table):
     return stride
 
 
-def _stream_of(stream, *made):
-    """The raw handle of a stream given by the caller. Tensors made for the
-    call are kept until that stream's work on them is done."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in made:
-        t.record_stream(stream)
+def _stream_object(stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _made(stream, shape, dtype, device):
+    """Memory for a call's result, of the stream that will write it: memory of
+    the current one may be what that stream's earlier work still uses."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(stream)):
+        return _empty(shape, dtype=dtype, device=device)
+
+
+def _stream_of(stream, *given):
+    """The raw handle of a stream given by the caller. Tensors given to be
+    written (or None) are kept until that stream's work on them is done."""
+    stream = _stream_object(stream)
+    for t in given:
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -200,9 +214,9 @@ def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=No
         raise ValueError("kind: 'rms' or 'layer' expected")
     device = x.get_device()
     _on_device(device, residual, weight, post_weight, post_bias, gate, bias, out, residual_out)
-    y = torch.empty_like(x) if out is None else out
-    r = torch.empty_like(x) if residual_out is None else residual_out
-    raw = _raw_stream(device) if stream is None else _stream_of(stream, y, r)
+    y = _made(stream, shape, _BF16, x.device) if out is None else out
+    r = _made(stream, shape, _BF16, x.device) if residual_out is None else residual_out
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, out, residual_out)
     rc = (_L or _lib()).mxfp4_residual_norm(
         x.data_ptr(), residual.data_ptr(), t, n, None if post_weight is None else post_weight.data_ptr(),
         _ptr(post_bias), _ptr(gate), gate_stride, scale, weight.data_ptr(), _ptr(bias), weight_offset, eps,
@@ -273,12 +287,12 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
         _ints(positions, tokens, "positions", device)
     _on_device(device, inv_freq, out)
     if out is None:
-        q = _empty((tokens, q_heads, d), dtype=_BF16, device=qkv.device)
+        q = _made(stream, (tokens, q_heads, d), _BF16, qkv.device)
     else:
         _need(out.dtype is _BF16 and out.shape == (tokens, q_heads, d) and out.is_contiguous(),
               "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
         q = out
-    raw = _raw_stream(device) if stream is None else _stream_of(stream, q)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, out)
     rc = (_L or _lib()).mxfp4_rope_append(
         qkv.data_ptr(), qkv.stride(0), q_heads, _ptr(positions), _ptr(inv_freq), rotary, interleaved, factor,
         cache.ref, batch.ref, q.data_ptr(), raw)
@@ -289,8 +303,12 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
 
 def attention_workspace(q_heads, cache, batch):
     """Scratch for attention calls with this cache and batch (any lengths)."""
+    return _attention_workspace(None, q_heads, cache, batch)
+
+
+def _attention_workspace(stream, q_heads, cache, batch):
     nbytes = _lib().mxfp4_attention_workspace_size(q_heads, cache.ref, batch.ref)
-    return _empty(max(nbytes, 256), dtype=torch.uint8, device=cache.k.device)
+    return _made(stream, max(nbytes, 256), torch.uint8, cache.k.device)
 
 
 def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None, out=None, lse=None, workspace=None,
@@ -311,7 +329,7 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
         _elsewhere()
     _on_device(device, tree_mask, out, lse, workspace)
     if out is None:
-        o = _empty(shape, dtype=_BF16, device=q.device)
+        o = _made(stream, shape, _BF16, q.device)
     else:
         _need(out.dtype is _BF16 and out.shape == shape and out.is_contiguous(),
               "out: contiguous bf16 [tokens, q_heads, head_dim] expected")
@@ -319,8 +337,8 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
     if lse is not None:
         _need(lse.dtype is _F32 and lse.shape == shape[:2] and lse.is_contiguous(),
               "lse: contiguous float32 [tokens, q_heads] expected")
-    ws = attention_workspace(heads, cache, batch) if workspace is None else workspace
-    raw = _raw_stream(device) if stream is None else _stream_of(stream, o, ws)
+    ws = _attention_workspace(stream, heads, cache, batch) if workspace is None else workspace
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, out, lse, workspace)
     rc = (_L or _lib()).mxfp4_attention(
         q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
         d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), o.data_ptr(), _ptr(lse),
@@ -332,7 +350,11 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
 
 def cache_workspace(sequences, num_pages, device="cuda"):
     """Scratch for cache_update calls of up to these sizes."""
-    return _empty(_lib().mxfp4_cache_workspace_size(sequences, num_pages), dtype=torch.uint8, device=device)
+    return _cache_workspace(None, sequences, num_pages, device)
+
+
+def _cache_workspace(stream, sequences, num_pages, device):
+    return _made(stream, _lib().mxfp4_cache_workspace_size(sequences, num_pages), torch.uint8, device)
 
 
 def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=None, stream=None):
@@ -354,12 +376,12 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     width, stride = block_table.shape[1], _row_stride(block_table)
     # Four allocations take 6 us of host time, one that is split and viewed 12.
     dev = block_table.device
-    table = _empty((n, width), dtype=_I32, device=dev)
-    lens = _empty(n, dtype=_I32, device=dev)
-    copies = _empty((n, 3), dtype=_I32, device=dev)
-    info = _empty(2, dtype=_I32, device=dev)
-    ws = cache_workspace(n, cache.num_pages, dev) if workspace is None else workspace
-    raw = _raw_stream(device) if stream is None else _stream_of(stream, table, lens, copies, info, ws)
+    table = _made(stream, (n, width), _I32, dev)
+    lens = _made(stream, n, _I32, dev)
+    copies = _made(stream, (n, 3), _I32, dev)
+    info = _made(stream, 2, _I32, dev)
+    ws = _cache_workspace(stream, n, cache.num_pages, dev) if workspace is None else workspace
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, workspace)
     rc = (_L or _lib()).mxfp4_cache_update(
         block_table.data_ptr(), stride, width, seq_lens.data_ptr(), old,
         parent.data_ptr(), _ptr(keep), grow.data_ptr(), n, cache.num_pages, cache.page_size, table.data_ptr(),
@@ -391,11 +413,11 @@ def cache_accept(cache, batch, path, n_accept, out=None, stream=None):
         _elsewhere()
     _on_device(device)
     if out is None:
-        lens = _empty(n, dtype=_I32, device=path.device)
+        lens = _made(stream, n, _I32, path.device)
     else:
         _ints(out, n, "out", device)
         lens = out
-    raw = _raw_stream(device) if stream is None else _stream_of(stream, lens)
+    raw = _raw_stream(device) if stream is None else _stream_of(stream, out)
     rc = (_L or _lib()).mxfp4_cache_accept(cache.ref, batch.ref, path.data_ptr(), length, n_accept.data_ptr(),
                                            lens.data_ptr(), raw)
     if rc:

@@ -191,6 +191,42 @@ def test_handles_over_two_devices_are_refused():
             mx.KVBatch(*args, tokens=4, max_q=2, max_seq=60)
 
 
+# ------------------------------------------------------------------- streams
+class Stream:
+    cuda_stream = 77
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_results_are_memory_of_the_stream_that_writes_them(name, library, monkeypatch):
+    """Memory of the current stream's pool may still be in use by that stream's earlier work, which another stream
+    does not wait for."""
+    import contextlib
+    current, made, kept = [0], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, current[0] = current[0], stream.cuda_stream
+        yield
+        current[0] = before
+
+    def empty(*shape, dtype, device):
+        made.append(current[0])
+        return torch.zeros(*shape, dtype=dtype)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(step, "_empty", empty)
+    monkeypatch.setattr(torch, "empty_like", lambda x: empty(x.shape, dtype=x.dtype, device=x.device))
+    monkeypatch.setattr(OnGpu, "record_stream", lambda self, s: kept.append(s.cuda_stream), raising=False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: None)
+    f, a = CALLS[name]()
+    f(**a, stream=Stream())  # what is given to be written is kept
+    given = [k for k in ("out", "residual_out", "lse", "workspace") if k in a]
+    assert kept == [77] * len(given) and library.calls[-1][1][-1] == 77
+    made.clear()
+    f(**{k: v for k, v in a.items() if k not in ("out", "residual_out", "workspace")}, stream=Stream())
+    assert set(made) <= {77} and (made or name == "copy")
+
+
 # ------------------------------------------------------------- rotary ramp
 @pytest.mark.parametrize("dim,base,trained,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 4096, 8.0), (64, 1e4, 32768, 4.0),
                                                      (128, 5e5, 8192, 16.0), (32, 1e4, 10 ** 6, 2.0)])
