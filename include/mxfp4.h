@@ -462,6 +462,7 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
  *   copies      device int32 [sequences][3]: source page, target page and
  *               rows of a page to copy (mxfp4_cache_copy), or -1, -1, 0
  *   info        device int32 [2]: pages left free; pages asked for in vain
+ *               (2^31 - 1 at most)
  *   workspace   at least mxfp4_cache_workspace_size() bytes, 256-byte
  *               aligned, contents on entry do not matter
  */

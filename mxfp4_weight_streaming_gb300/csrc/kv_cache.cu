@@ -7,6 +7,8 @@
 // contiguous 16-byte vectors, a block per page or request, head and K or V of
 // a layer. Update and copy of 32 beams in 24 layers (93 MB moved each way) take
 // 21 us together, accept and update of 8 requests in 16 layers 13 us.
+#include <climits>
+
 #include "step_launch.h"
 
 #include "step_common.cuh"
@@ -38,25 +40,26 @@ __host__ __device__ UpdateSpace update_space(void* ws, int64_t sequences, int64_
 }
 
 // Exclusive sum over the block, and the block's total.
-__device__ __forceinline__ int block_scan(int v, int* total, int* part) {
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* total, T* part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
+    T inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        const T t = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += t;
     }
     __syncthreads();
     if (lane == 31) part[warp] = inc;
     __syncthreads();
-    int w = part[lane];
+    T w = part[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, w, o);
+        const T t = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += t;
     }
     *total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
+    const T before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
     return inc - v + (warp ? before : 0);
 }
 
@@ -64,6 +67,7 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* part) {
 // not show in the result.
 __global__ void __launch_bounds__(kUpdateThreads) cache_update_kernel(CacheUpdateArgs a) {
     __shared__ int part[32];
+    __shared__ int64_t part64[32];
     const UpdateSpace s = update_space(a.workspace, a.sequences, a.num_pages);
     const int page = 1 << a.page_shift, tid = threadIdx.x;
     pdl_wait_previous();
@@ -110,8 +114,10 @@ __global__ void __launch_bounds__(kUpdateThreads) cache_update_kernel(CacheUpdat
         }
     }
     __syncthreads();
-    // Pages each sequence asks for, and where its share of the free ones begins.
-    int need_total = 0;
+    // Pages each sequence asks for, and where its share of the free ones begins
+    // (at the pool's size at most, where none are left). The sum is 64 bits:
+    // 65,536 sequences may ask for 2^24 pages each.
+    int64_t need_total = 0;
     for (int i0 = 0; i0 < a.sequences; i0 += kUpdateThreads) {
         const int i = i0 + tid;
         int need = 0, copy = 0;
@@ -120,10 +126,10 @@ __global__ void __launch_bounds__(kUpdateThreads) cache_update_kernel(CacheUpdat
             if (last >= 0) copy = !(s.refs[last] == s.writers[last] && s.lowest[last] == i);
             need = copy + ((s.want[i] + page - 1) >> a.page_shift) - ((s.base[i] + page - 1) >> a.page_shift);
         }
-        int total;
-        const int off = block_scan(need, &total, part);
+        int64_t total;
+        const int64_t off = need_total + block_scan<int64_t>(need, &total, part64);
         if (i < a.sequences) {
-            s.offset[i] = need_total + off;
+            s.offset[i] = static_cast<int>(min(off, static_cast<int64_t>(a.num_pages)));
             if (!copy) s.last[i] = -1;
         }
         need_total += total;
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(kUpdateThreads) cache_update_kernel(CacheUpdat
         const int p = p0 + tid;
         const int is_free = p < a.num_pages && s.refs[p] == 0;
         int total;
-        const int rank = free_total + block_scan(is_free, &total, part);
+        const int rank = free_total + block_scan<int>(is_free, &total, part);
         if (is_free) s.by_rank[rank] = p;
         free_total += total;
     }
@@ -161,9 +167,9 @@ __global__ void __launch_bounds__(kUpdateThreads) cache_update_kernel(CacheUpdat
         a.copies[3 * i + 2] = copied ? base & (page - 1) : 0;
     }
     if (tid == 0) {
-        const int given = min(need_total, free_total);
-        a.info[0] = free_total - given;
-        a.info[1] = need_total - given;
+        const int64_t given = min(need_total, static_cast<int64_t>(free_total));
+        a.info[0] = free_total - static_cast<int>(given);
+        a.info[1] = static_cast<int>(min(need_total - given, static_cast<int64_t>(INT_MAX)));
     }
 }
 

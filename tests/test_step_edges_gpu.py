@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gpu_cases import lib
-from step_cases import gen, randn
+from step_cases import gen, ints, randn
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -26,3 +26,22 @@ def test_results_on_another_stream_are_not_memory_of_the_current_ones_work():
     y, r = mx.residual_norm(x, res, w, stream=other)
     torch.cuda.synchronize()
     assert torch.equal(y, y0) and torch.equal(r, r0)
+
+
+# --------------------------------------------------------------------- pages
+def test_more_pages_asked_for_than_32_bits_count():
+    """130 sequences that ask for 2^24 - 1 pages each, 2^31 in all, of a pool of 9: the first takes them, the others
+    get nothing, and none reads beyond the list of free pages."""
+    mx = lib()
+    n, width = 130, (1 << 24) - 1
+    pool = torch.empty(9, 1, 16, 64, dtype=BF16, device="cuda")
+    old = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    grow = 2 ** 31 - 1
+    table, lens, copies, info = mx.cache_update(mx.KVCache(pool, pool), old, ints([0]), ints([-1] * n), None,
+                                                ints([grow] * n))
+    assert table[0, :9].tolist() == list(range(9)) and int((table[0, 9:] != -1).sum()) == 0
+    assert all(int((row != -1).sum()) == 0 for row in table[1:])
+    assert lens.tolist() == [9 * 16] + [0] * (n - 1) and copies.tolist() == [[-1, -1, 0]] * n
+    assert info.tolist() == [0, 2 ** 31 - 1]
+    small = mx.cache_update(mx.KVCache(pool, pool), old[:, :4].contiguous(), ints([0]), ints([-1] * 3), None, ints([40] * 3))
+    assert small[3].tolist() == [0, 0] and small[1].tolist() == [40] * 3
