@@ -423,7 +423,8 @@ int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const in
  * whatever it holds (NaN and infinities included).
  *   q          device bf16, rows of q_heads * head_dim, q_stride elements
  *              apart, 16-byte aligned, q_stride % 8 == 0
- *   q_heads    a multiple of kv_heads, at most 128 * kv_heads
+ *   q_heads    a multiple of kv_heads, at most 128 * kv_heads; tokens *
+ *              q_heads / kv_heads at most 2^31 - 256
  *   softcap    0: none;  window 0: none
  *   tree_mask  device uint64 [tokens] or NULL; max_q <= 64
  *   out        device bf16 [tokens, q_heads, head_dim], 16-byte aligned;

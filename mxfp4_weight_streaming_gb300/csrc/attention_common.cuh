@@ -43,8 +43,8 @@ inline Divisor divisor(int d) {
     return v;
 }
 
-// Cut of one call. Rows of a request, n * group, stay below 2^31 (2^24 tokens
-// and 128 heads a group at most).
+// Cut of one call. Rows of a request, n * group, are at most 2^31 - 256 (the
+// entry point refuses more).
 struct Cut {
     int group;       // query heads per KV head
     Divisor by_group;

@@ -181,7 +181,9 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
         return MXFP4_ERR_INVALID_ARG;
     if (int rc = cache_status(cache)) return rc;
     if (int rc = batch_status(batch)) return rc;
-    if (q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads || (tree_mask && batch->max_q > 64))
+    // The kernels count a request's rows, rounded up to a row tile, in an int.
+    if (q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads || (tree_mask && batch->max_q > 64) ||
+        static_cast<int64_t>(batch->tokens) * (q_heads / cache->kv_heads) > (int64_t(1) << 31) - 256)
         return MXFP4_ERR_SHAPE;
     if (q_stride < static_cast<int64_t>(q_heads) * cache->head_dim) return MXFP4_ERR_INVALID_ARG;
     if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8))
