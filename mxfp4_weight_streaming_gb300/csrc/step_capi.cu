@@ -207,7 +207,9 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
     a.e4m3 = cache->dtype == MXFP4_KV_E4M3;
     a.scale = scale;
     a.softcap = softcap;
-    a.window = window;
+    // Sequences are cut to 2^30 tokens (batch_view), which a longer window never
+    // leaves; the kernels' differences with it then stay within an int.
+    a.window = window < (1 << 30) ? window : 0;
     return launched(mxfp4::launch_attention(a, cache_view(*cache), batch_view(*batch, cache->page_size), caps.num_sms,
                                             static_cast<cudaStream_t>(stream)));
 }

@@ -96,3 +96,13 @@ def test_nan_scale_of_a_head(news):
     ref, _, mag = attention_ref(pg, q, 0.125)
     check(out[:, :4], ref[:, :4], attention_bound(ref, mag, E4M3)[:, :4], "the other KV head")
     assert torch.isnan(out[1:, 4:].float()).all() and (out[0] == 0).all()
+
+
+# ------------------------------------------------------------------- bounds
+@pytest.mark.parametrize("window", [2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("heads", [1, 4, 16])
+def test_windows_longer_than_any_sequence(window, dtype, heads):
+    """Also where the first queries lie before their sequence."""
+    pg = Paged(heads, [6, 0, 40], 1, 64, 16, dtype)
+    run(pg, [10, 3, 2], heads, window=window, what=f"window {window}")
