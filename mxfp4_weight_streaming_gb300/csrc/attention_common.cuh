@@ -246,7 +246,10 @@ cudaError_t launch_join(const Params& p, bool e4m3, bool from_tc, int ctas, cuda
 inline int ctas_for(const Params& p, int64_t max_rows, int max_seq, int most) {
     const int64_t rows = (max_rows + (1 << p.cut.row_shift) - 1) >> p.cut.row_shift;
     const int64_t keys = (static_cast<int64_t>(max_seq) >> p.cut.key_shift) + 2;
-    const int64_t tiles = rows * keys * p.cut.kv_heads * p.batch.batch;
+    // Any int32 bounds will do, so the product is cut on the way.
+    int64_t tiles = rows;
+    for (const int64_t f : {keys, static_cast<int64_t>(p.cut.kv_heads), static_cast<int64_t>(p.batch.batch)})
+        tiles = tiles < most ? tiles * f : most;
     return tiles < most ? static_cast<int>(tiles) : most;
 }
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_cases import lib
-from step_cases import E4M3, Paged, attention_bound, attention_ref, check, gen, randn
+from step_cases import E4M3, Paged, attention_bound, attention_ref, check, gen, ints, randn
 from test_attention_gpu import run
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +106,18 @@ def test_windows_longer_than_any_sequence(window, dtype, heads):
     """Also where the first queries lie before their sequence."""
     pg = Paged(heads, [6, 0, 40], 1, 64, 16, dtype)
     run(pg, [10, 3, 2], heads, window=window, what=f"window {window}")
+
+
+def test_bounds_far_above_the_lengths():
+    """max_q and max_seq size the kernels; any int32 will do."""
+    mx = lib()
+    lens = [(i * 7) % 90 + 3 for i in range(1024)]
+    pg = Paged(31, lens, 8, 64, 16)
+    news = [i % 3 for i in range(1024)]
+    tight = pg.batch(mx, news)
+    start, most = ints(pg.start), 2 ** 31 - 1
+    loose = mx.KVBatch(start, ints(lens), pg.table, tokens=pg.start[-1], max_q=most, max_seq=most)
+    q = randn(gen(4), pg.start[-1], 64, 64)
+    a, b = mx.attention(q, pg.cache(mx), tight), mx.attention(q, pg.cache(mx), loose)
+    # Two kernels: each off by what attention_bound allows, 2^-7 + 2^-12 of the largest |v| (below 6) at most.
+    assert (a.double() - b.double()).abs().max() < 2 * (2 ** -7 + 2 ** -12) * 6
