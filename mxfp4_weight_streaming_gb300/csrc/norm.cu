@@ -154,8 +154,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[c][j] = fmaf(p.scale, u[c][j], r[c][j]);
         }
-        const int next = t + gridDim.x;
-        if (next < p.tokens) load_row(next);
+        // Compared as a distance: t + gridDim.x may pass 2^31.
+        const bool more = static_cast<int>(gridDim.x) < p.tokens - t;
+        const int next = more ? t + static_cast<int>(gridDim.x) : t;
+        if (more) load_row(next);
 #pragma unroll
         for (int c = 0; c < CH; ++c) R::store_chunk(p.r_out + row, n, c, r[c]);
         const float f = centre_and_factor(r, 2);
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(
             }
             R::store_chunk(p.y + row, n, c, r[c]);
         }
-        if (next >= p.tokens) break;
+        if (!more) break;
         t = next;
         __syncthreads();  // the sums' slots are free again
     }

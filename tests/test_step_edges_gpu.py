@@ -45,3 +45,21 @@ def test_more_pages_asked_for_than_32_bits_count():
     assert info.tolist() == [0, 2 ** 31 - 1]
     small = mx.cache_update(mx.KVCache(pool, pool), old[:, :4].contiguous(), ints([0]), ints([-1] * 3), None, ints([40] * 3))
     assert small[3].tolist() == [0, 0] and small[1].tolist() == [40] * 3
+
+
+# --------------------------------------------------------------------- norms
+def test_residual_norm_of_as_many_rows_as_an_int_counts():
+    """2^31 - 1 rows of one element: y = sign(r) but for eps, r = x + residual."""
+    mx = lib()
+    t = 2 ** 31 - 1
+    x = torch.empty(t, 1, dtype=BF16, device="cuda")
+    x.view(-1)[:-1].view(-1, 2).copy_(torch.tensor([1.0, -3.0], dtype=BF16, device="cuda"))
+    x[-1] = 5.0
+    w = torch.full((1,), 2.0, dtype=BF16, device="cuda")
+    y, r = mx.residual_norm(x, x, w, out=torch.full_like(x, 9.0), residual_out=torch.full_like(x, 9.0))
+    torch.cuda.synchronize()
+    for got, even, odd, last in ((r, 2.0, -6.0, 10.0), (y, 2.0, -2.0, 2.0)):
+        pairs = got.view(-1)[:-1].view(-1, 2)
+        for part in pairs.split(1 << 27):
+            assert bool((part[:, 0] == even).all()) and bool((part[:, 1] == odd).all())
+        assert float(got[-1]) == last
