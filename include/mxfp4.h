@@ -483,10 +483,11 @@ int mxfp4_cache_copy(const mxfp4_kv_cache_t* cache, const int32_t* copies, int s
  * After a verify step: moves the K and V rows of the accepted draft path to
  * the front of each request's new tokens, in every layer. Row i of the new
  * tokens becomes row path[b][i] for i < n_accept[b]; entries outside the new
- * tokens move nothing.
+ * tokens, or of tokens that lie before the sequence, move nothing.
  *   path       device int32 [batch][path_len], path_len 1 .. 64
- *   n_accept   device int32 [batch], cut to [0, new tokens]
- *   lens_out   device int32 [batch], not seq_lens: tokens before the step + n_accept
+ *   n_accept   device int32 [batch], cut to [0, new tokens] and to path_len
+ *   lens_out   device int32 [batch], not seq_lens: seq_lens - new tokens +
+ *              n_accept, not below 0
  */
 int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* batch, const int32_t* path,
                        int path_len, const int32_t* n_accept, int32_t* lens_out, void* stream);

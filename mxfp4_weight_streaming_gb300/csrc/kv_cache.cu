@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kMoveThreads) cache_accept_kernel(PoolView poo
     const int b = blockIdx.x;
     int first, n, seq;
     request_extent(bt, b, first, n, seq);
-    const int start = max(seq - n, 0);
-    const int took = min(max(n_accept[b], 0), min(path_len, seq - start));
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) lens_out[b] = start + took;
+    const int start = seq - n;  // of new token 0; below 0 it is not in the cache
+    const int took = min(max(n_accept[b], 0), min(path_len, n));
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) lens_out[b] = max(start + took, 0);
     const int layer = blockIdx.z >> 1;
     char* base = static_cast<char*>((blockIdx.z & 1) ? pool.v : pool.k) + layer * pool.layer_stride +
                  ((static_cast<int64_t>(blockIdx.y) << pool.page_shift) * pool.row_bytes);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_accept_kernel(PoolView poo
     uint32_t have = 0;
     const int mask = (1 << pool.page_shift) - 1;
     auto row_ptr = [&](int at) -> uint4* {
-        const int page = page_of(bt, b, at, pool.page_shift, pool.num_pages);
+        const int page = at < 0 ? -1 : page_of(bt, b, at, pool.page_shift, pool.num_pages);
         return page < 0 ? nullptr
                         : reinterpret_cast<uint4*>(base + page * pool.page_stride +
                                                    static_cast<int64_t>(at & mask) * pool.row_bytes);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_accept_kernel(PoolView poo
         const int v = h * kMoveThreads + threadIdx.x, i = v / vecs;
         if (i >= took) continue;
         const int from = path[static_cast<int64_t>(b) * path_len + i];
-        if (from < 0 || from >= seq - start || from == i) continue;
+        if (from < 0 || from >= n || from == i) continue;
         const uint4* p = row_ptr(start + from);
         if (!p) continue;
         held[h] = p[v % vecs];

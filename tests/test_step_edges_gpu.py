@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gpu_cases import lib
-from step_cases import gen, ints, randn
+from step_cases import E4M3, Paged, gen, ints, randn
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -63,3 +63,29 @@ def test_residual_norm_of_as_many_rows_as_an_int_counts():
         for part in pairs.split(1 << 27):
             assert bool((part[:, 0] == even).all()) and bool((part[:, 1] == odd).all())
         assert float(got[-1]) == last
+
+
+# --------------------------------------------------------- accepted drafts
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_accept_where_the_sequence_is_shorter_than_the_chunk(dtype):
+    """New token i lies at seq_len - n + i here too: those below 0 are not in the cache, and move nothing."""
+    mx = lib()
+    lens, news = [6, 0, 20], [10, 3, 4]
+    pg = Paged(2, lens, 2, 64, 16, dtype, layers=2)
+    for pool in (pg.kp, pg.vp):
+        b = pool.view(torch.uint8)
+        b.copy_(torch.randint(0, 255, b.shape, dtype=torch.uint8, device="cuda", generator=gen(3)))
+    path = torch.tensor([[0, 1, 2, 3, 9, 7, 5, 4], [0, 1, 2, 0, 0, 0, 0, 0], [0, 2, 3, 0, 0, 0, 0, 0]], dtype=torch.int32)
+    took = [8, 3, 3]
+    old = {n: getattr(pg, n).view(torch.uint8).clone() for n in ("kp", "vp")}
+    out = mx.cache_accept(pg.cache(mx), pg.batch(mx, news), path.cuda(), ints(took))
+    assert out.tolist() == [6 - 10 + 8, 0, 19]
+    for name in ("kp", "vp"):
+        want = old[name].clone()
+        for b in range(3):
+            first = lens[b] - news[b]
+            for i in range(took[b]):
+                to, fr = first + i, first + int(path[b, i])
+                if to >= 0 and fr >= 0:
+                    want[:, pg.table[b, to // 16], :, to % 16] = old[name][:, pg.table[b, fr // 16], :, fr % 16]
+        assert torch.equal(getattr(pg, name).view(torch.uint8), want)
