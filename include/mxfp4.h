@@ -403,8 +403,8 @@ int mxfp4_residual_norm(const void* x, const void* residual, int64_t tokens, int
  *   inv_freq     device float32 [rotary_dim / 2]
  *   rotary_dim   even, 0 .. head_dim (0: nothing turns, inv_freq may be NULL)
  *   q_out        device bf16 [tokens, q_heads, head_dim], 16-byte aligned
- * E4M3 caches store value / scale, rounded to nearest even and saturating at
- * 448. Rows of qkv beyond q_start[batch] are left out.
+ * E4M3 caches store value / scale, the fp32 quotient rounded to nearest even
+ * and saturating at 448. Rows of qkv beyond q_start[batch] are left out.
  */
 int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const int32_t* positions,
                       const float* inv_freq, int rotary_dim, int interleaved, float factor,

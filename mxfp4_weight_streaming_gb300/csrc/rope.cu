@@ -178,9 +178,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(RopeParams
             const int64_t to = page * cv.page_stride + ((kh << cv.page_shift) + slot) * D + d0;
             if constexpr (E4M3) {
                 const float* sc = is_v ? cv.v_scale : cv.k_scale;
-                const float inv = sc ? __frcp_rn(sc[kh]) : 1.f;
+                // A division each: a product with 1 / scale lands on the other side
+                // of a middle between two codes now and then, and scales of the
+                // form largest / 448 put many quotients there.
+                const float scale = sc ? sc[kh] : 1.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] *= inv;
+                for (int j = 0; j < 8; ++j) o[j] = __fdiv_rn(o[j], scale);
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? cv.v : cv.k) + to) = pack8_e4m3(o);
             } else {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? cv.v : cv.k) + to);

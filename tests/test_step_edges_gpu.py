@@ -89,3 +89,23 @@ def test_accept_where_the_sequence_is_shorter_than_the_chunk(dtype):
                 if to >= 0 and fr >= 0:
                     want[:, pg.table[b, to // 16], :, to % 16] = old[name][:, pg.table[b, fr // 16], :, fr % 16]
         assert torch.equal(getattr(pg, name).view(torch.uint8), want)
+
+
+# ------------------------------------------------------------- E4M3 rounding
+def test_e4m3_rows_are_divided_by_their_scale():
+    """The stored byte is the quotient's, not that of a product with 1 / scale: scales of the form
+    largest / 448, as a calibration gives them, put many quotients on the middle between two codes."""
+    mx = lib()
+    mant = (torch.arange(128, dtype=torch.int32) + 0x3F80).to(torch.int16).view(BF16)  # [1, 2)
+    scales = (mant.float() / 448).cuda()
+    heads = 128
+    x = torch.stack([mant, -mant * 2 ** -3, mant * 2 ** -9, mant * 8]).cuda()  # [4 tokens, 128]
+    pool = torch.zeros(2, heads, 16, 128, dtype=torch.uint8, device="cuda").view(E4M3)
+    vpool = torch.zeros(2, heads, 16, 128, dtype=torch.uint8, device="cuda").view(E4M3)
+    cache = mx.KVCache(pool, vpool, scales, scales)
+    qkv = torch.cat([x[:, None], x[:, None].expand(4, 2 * heads, 128)], 1).reshape(4, -1).contiguous()
+    batch = mx.KVBatch(ints([0, 4]), ints([4]), ints([[1]]), tokens=4, max_q=4, max_seq=4)
+    mx.rope_append(qkv, 1, None, cache, batch)
+    want = (x.float()[None] / scales[:, None, None]).clamp(-448, 448).to(E4M3)  # [heads, 4, 128]
+    for got in (pool, vpool):
+        assert torch.equal(got.view(torch.uint8)[1, :, :4], want.view(torch.uint8))
