@@ -92,6 +92,11 @@ def _ints(t, count, name, device):
         _elsewhere()
 
 
+def _strides(t):
+    """A tensor's strides, None where there is one entry only and its stride says nothing."""
+    return [stride if size > 1 else None for size, stride in zip(t.shape, t.stride())]
+
+
 def _row_stride(table):
     """Entries between a block table's rows. A row that several requests
     share by expand() has a stride of 0, which the C side takes as dense."""
@@ -135,15 +140,15 @@ class KVCache:
     one layer: `cache.layer(i)`."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        _need(k.dim() in (4, 5) and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
+        _need(k.dim() in (4, 5) and k.shape == v.shape and k.dtype == v.dtype and _strides(k) == _strides(v),
               "k and v: pools of one shape, type and strides expected")
         _need(k.is_cuda and v.is_cuda and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
               "k and v: bf16 or float8_e4m3fn CUDA tensors expected")
         pages, heads, page, dim = k.shape[-4:]
-        _need(k.stride(-1) == 1 and k.stride(-2) == dim and k.stride(-3) == page * dim, "a page has to be dense")
+        strides = _strides(k)
+        _need(all(have in (want, None) for have, want in zip(strides[-3:], (page * dim, dim, 1))), "a page has to be dense")
         # A stride of 0 (an expanded tensor) would mean "dense" to the C side.
-        for d in range(k.dim() - 3):
-            _need(k.shape[d] == 1 or k.stride(d) >= heads * page * dim, "pages and layers may not share memory")
+        _need(all(have is None or have >= heads * page * dim for have in strides[:-3]), "pages and layers may not share memory")
         e4m3 = k.dtype == torch.float8_e4m3fn
         for sc in (k_scale, v_scale):
             _need(sc is None or (e4m3 and sc.is_cuda and sc.dtype == torch.float32 and sc.shape == (heads,)
@@ -154,8 +159,8 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.layers = k.shape[0] if k.dim() == 5 else 1
-        self.struct = KVCacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(-4),
-                                    k.stride(0) if k.dim() == 5 else 0, pages, self.layers, heads, page, dim,
+        self.struct = KVCacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), strides[-4] or heads * page * dim,
+                                    (strides[0] or 0) if k.dim() == 5 else 0, pages, self.layers, heads, page, dim,
                                     KV_E4M3 if e4m3 else KV_BF16, 0)
         self.ref = ctypes.addressof(self.struct)
 
@@ -177,7 +182,7 @@ class KVBatch:
         _ints(seq_lens, b, "seq_lens", device)
         _ints(q_start, b + 1, "q_start", device)
         _need(block_table.is_cuda and block_table.dtype == torch.int32 and block_table.dim() == 2
-              and block_table.shape[0] == b and block_table.stride(1) == 1,
+              and block_table.shape[0] == b and _strides(block_table)[1] in (1, None),
               "block_table: int32 CUDA tensor [batch, width] expected")
         self.q_start, self.seq_lens, self.block_table = q_start, seq_lens, block_table
         self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), int(max_q), int(max_seq)
@@ -203,7 +208,7 @@ def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=No
             raise ValueError("weights: contiguous bf16 [n] expected")
     gate_stride = 0
     if gate is not None:
-        _need(gate.dtype is _BF16 and gate.shape in ((n,), (t, n)) and gate.stride(-1) == 1,
+        _need(gate.dtype is _BF16 and gate.shape in ((n,), (t, n)) and (gate.stride(-1) == 1 or n == 1),
               "gate: bf16 [n] or [tokens, n] expected")
         if gate.dim() == 2:
             gate_stride = gate.stride(0) if t > 1 else n
@@ -370,7 +375,7 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     if keep is not None:
         _ints(keep, n, "keep", device)
     if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.shape[0] != old or \
-            block_table.stride(1) != 1 or not block_table.is_cuda:
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1) or not block_table.is_cuda:
         raise ValueError("block_table: int32 CUDA tensor [old, width] expected")
     _on_device(device, workspace)
     width, stride = block_table.shape[1], _row_stride(block_table)

@@ -227,6 +227,34 @@ def test_results_are_memory_of_the_stream_that_writes_them(name, library, monkey
     assert set(made) <= {77} and (made or name == "copy")
 
 
+# -------------------------------------------------------- sizes of one
+def test_strides_of_single_entries_do_not_matter():
+    """A dimension of size 1 may carry any stride: out of a transpose, or of a slice of a larger pool."""
+    k = torch.zeros(8, 16, 1, 64, dtype=BF16).transpose(1, 2)  # one KV head: stride(1) is a row's
+    v = torch.zeros(8, 1, 16, 64, dtype=BF16)
+    c = mx.KVCache(OnGpu(k), OnGpu(v)).struct
+    assert k.stride() != v.stride() and (c.page_stride, c.kv_heads, c.layer_stride) == (16 * 64, 1, 0)
+    one_page = torch.zeros(4, 2, 16, 64, dtype=BF16).as_strided((1, 2, 16, 64), (8, 1024, 64, 1))
+    c = mx.KVCache(OnGpu(one_page), OnGpu(torch.zeros(1, 2, 16, 64, dtype=BF16))).struct
+    assert c.num_pages == 1 and c.page_stride in (0, 2 * 16 * 64)
+    one_layer = torch.zeros(1, 8, 2, 16, 64, dtype=BF16).as_strided((1, 8, 2, 16, 64), (4, 2048, 1024, 64, 1))
+    c = mx.KVCache(*[OnGpu(one_layer)] * 2).struct
+    assert c.layers == 1 and c.layer_stride in (0, 8 * 2048)
+    with pytest.raises(ValueError):  # strides that matter still have to agree
+        mx.KVCache(OnGpu(torch.zeros(8, 2, 2, 16, 64, dtype=BF16)[:, 0]), OnGpu(torch.zeros(8, 2, 16, 64, dtype=BF16)))
+    with pytest.raises(ValueError):
+        mx.KVCache(*[OnGpu(torch.zeros(8, 16, 2, 64, dtype=BF16).transpose(1, 2))] * 2)
+
+
+def test_a_table_of_one_column_and_a_gate_of_one_element():
+    table = torch.zeros(40, dtype=I32).as_strided((3, 1), (4, 7))
+    assert mx.KVBatch(ints(4), ints(3), OnGpu(table), tokens=3, max_q=1, max_seq=16).struct.table_stride == 4
+    f, a = norm_call(x=bf16(4, 1), residual=bf16(4, 1), weight=bf16(1), post_weight=None, post_bias=None, bias=None,
+                     gate=OnGpu(torch.zeros(4, 8, dtype=BF16).as_strided((4, 1), (8, 3))), out=bf16(4, 1),
+                     residual_out=bf16(4, 1))
+    f(**a)
+
+
 # ------------------------------------------------------------- rotary ramp
 @pytest.mark.parametrize("dim,base,trained,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 4096, 8.0), (64, 1e4, 32768, 4.0),
                                                      (128, 5e5, 8192, 16.0), (32, 1e4, 10 ** 6, 2.0)])
