@@ -418,7 +418,10 @@ int mxfp4_rope_append(const void* qkv, int64_t qkv_stride, int q_heads, const in
  * A query at cache index c sees j <= c; with a window, j > c - window too.
  * tree_mask replaces j <= c among the new tokens of a request: bit j of a
  * query's word says that it sees new token j (a draft tree's ancestors and
- * itself); what lies before the new tokens stays visible. A query that sees
+ * itself); what lies before the new tokens stays visible. A window counts
+ * cache indices, for drafts of a tree too: a draft at index i and depth d < i
+ * loses the i - d oldest keys that decoding it alone would see.
+ * mxfp4_attention_at counts from the drafts' positions. A query that sees
  * nothing gives 0 (lse -inf). What is not visible has no part in a result,
  * whatever it holds (NaN and infinities included).
  *   q          device bf16, rows of q_heads * head_dim, q_stride elements
@@ -440,6 +443,20 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
                     const mxfp4_kv_batch_t* batch, float scale, float softcap, int window,
                     const uint64_t* tree_mask, void* out, float* lse, void* workspace, size_t workspace_bytes,
                     void* stream);
+
+/*
+ * The same with the drafts' positions, as mxfp4_rope_append takes them: a
+ * window leaves out what lies before the new tokens at cache index
+ * <= position - window. Which of the new tokens a query sees is the
+ * tree_mask's alone (one that the window has left is not in it).
+ *   positions  device int32 [tokens], each cut to the cache indices of its
+ *              request's new tokens (first new token + depth in the tree lies
+ *              among them); needs tree_mask; NULL = mxfp4_attention
+ */
+int mxfp4_attention_at(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv_cache_t* cache,
+                       const mxfp4_kv_batch_t* batch, float scale, float softcap, int window,
+                       const uint64_t* tree_mask, const int32_t* positions, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /*
  * The cache's pages from one step to the next, in one call: fork, reorder,

@@ -34,8 +34,8 @@ MXFP4_ERR_TIMEOUT = 6
 
 EXPORTED = ["mxfp4_strerror", "mxfp4_quantize", "mxfp4_linear", "mxfp4_linear_plan", "mxfp4_moe_workspace_size",
             "mxfp4_moe", "mxfp4_last_device_status", "mxfp4_residual_norm", "mxfp4_rope_append",
-            "mxfp4_attention_workspace_size", "mxfp4_attention", "mxfp4_cache_workspace_size", "mxfp4_cache_update",
-            "mxfp4_cache_copy", "mxfp4_cache_accept"]
+            "mxfp4_attention_workspace_size", "mxfp4_attention", "mxfp4_attention_at", "mxfp4_cache_workspace_size",
+            "mxfp4_cache_update", "mxfp4_cache_copy", "mxfp4_cache_accept"]
 
 _lib = None
 
@@ -96,6 +96,8 @@ def load() -> ctypes.CDLL:
     L.mxfp4_attention_workspace_size.argtypes = [I, P, P]
     L.mxfp4_attention.restype = I
     L.mxfp4_attention.argtypes = [P, I64, I, P, P, F, F, I, P, P, P, P, S, P]
+    L.mxfp4_attention_at.restype = I
+    L.mxfp4_attention_at.argtypes = [P, I64, I, P, P, F, F, I, P, P, P, P, P, S, P]
     L.mxfp4_cache_workspace_size.restype = S
     L.mxfp4_cache_workspace_size.argtypes = [I64, I64]
     L.mxfp4_cache_update.restype = I

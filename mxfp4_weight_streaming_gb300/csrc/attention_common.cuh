@@ -53,6 +53,7 @@ struct Cut {
     int key_shift;   // keys per unit of work
     int window;      // 0: none
     bool tree;
+    bool placed;     // windows count from Params::positions, not from the cache index
     int min_share;   // units a CTA takes at least
 };
 
@@ -62,7 +63,7 @@ __device__ __forceinline__ void item_keys(const Cut& c, int n, int seq, int rt, 
     const int tok0 = c.by_group.div(rt << c.row_shift);
     const int tok1 = min(n - 1, c.by_group.div((rt << c.row_shift) + (1 << c.row_shift) - 1));
     end = c.tree ? seq : max(seq - n + tok1 + 1, 0);
-    begin = c.window ? max(seq - n + tok0 - c.window + 1, 0) : 0;
+    begin = c.window ? max(seq - n + (c.placed ? 0 : tok0) - c.window + 1, 0) : 0;
     end = max(end, begin);
 }
 
@@ -220,11 +221,18 @@ struct ScoreMap {
     }
 };
 
+// Where a query's window counts from, by its position (cut to the cache indices
+// of the new tokens [start, seq), and so that it leaves none of those out).
+__device__ __forceinline__ int window_from(const int* position, int start, int seq, int window) {
+    return min(min(max(load_word(position), start), seq - 1), start + window - 1);
+}
+
 // What the kernels take.
 struct Params {
     const __nv_bfloat16* q;
     int64_t q_stride;
     const unsigned long long* tree_mask;
+    const int* positions;  // of the queries, where a window counts from them: null unless cut.placed
     __nv_bfloat16* out;
     float* lse;
     void* ws;

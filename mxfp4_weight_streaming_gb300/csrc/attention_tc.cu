@@ -812,11 +812,13 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             }
             const int tr = (SPLIT ? 0 : wg * 128) + r;  // row in the row tile
             const bool in = tr < g.rows;
-            const int tok = cut.by_group.div(g.row0 + (in ? tr : 0)), pos = g.start + tok;
+            const int tok = cut.by_group.div(g.row0 + (in ? tr : 0));
+            int pos = g.start + tok;
+            if (cut.placed && in) pos = window_from(p.positions + g.q0 + tok, g.start, g.end, cut.window);
             // Keys below `open` are visible to every row of the stream (without
             // a window); keys from `all_from` on have left no row's window.
             const int open = cut.tree ? g.start : g.start + cut.by_group.div(g.row0 + (SPLIT ? 0 : wg * 128)) + 1;
-            const int all_from = g.start + cut.by_group.div(g.row0 + g.rows - 1) - cut.window + 1, open_end = min(open, g.end);
+            const int all_from = g.end - cut.window, open_end = min(open, g.end);
             // This row's first and last visible key.
             const int first = max(g.begin, cut.window ? pos - cut.window + 1 : 0);
             const int last = in ? min(cut.tree ? g.end - 1 : pos, g.end - 1) : -1;

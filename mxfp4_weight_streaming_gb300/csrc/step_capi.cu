@@ -97,6 +97,49 @@ mxfp4::PoolView pool_view(const mxfp4_kv_cache_t& c) {
 
 int caps_of(mxfp4::DeviceCaps* caps) { return mxfp4::device_caps(caps); }
 
+int attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv_cache_t* cache,
+              const mxfp4_kv_batch_t* batch, float scale, float softcap, int window, const uint64_t* tree_mask,
+              const int32_t* positions, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (positions && !tree_mask) return MXFP4_ERR_INVALID_ARG;
+    if (!q || !out || q_heads <= 0 || window < 0 || !(softcap >= 0.f) || std::isinf(softcap) || !std::isfinite(scale))
+        return MXFP4_ERR_INVALID_ARG;
+    if (int rc = cache_status(cache)) return rc;
+    if (int rc = batch_status(batch)) return rc;
+    // The kernels count a request's rows, rounded up to a row tile, in an int.
+    if (q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads || (tree_mask && batch->max_q > 64) ||
+        static_cast<int64_t>(batch->tokens) * (q_heads / cache->kv_heads) > (int64_t(1) << 31) - 256)
+        return MXFP4_ERR_SHAPE;
+    if (q_stride < static_cast<int64_t>(q_heads) * cache->head_dim) return MXFP4_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8) ||
+        !aligned(positions, 4))
+        return MXFP4_ERR_ALIGN;
+    if (!workspace) return MXFP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MXFP4_ERR_ALIGN;
+    if (workspace_bytes < mxfp4_attention_workspace_size(q_heads, cache, batch)) return MXFP4_ERR_WORKSPACE;
+    mxfp4::DeviceCaps caps;
+    if (int rc = caps_of(&caps)) return rc;
+    mxfp4::AttentionArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+    a.positions = positions;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status = caps.status;
+    a.q_heads = q_heads;
+    a.max_q = batch->max_q;
+    a.max_seq = batch->max_seq;
+    a.e4m3 = cache->dtype == MXFP4_KV_E4M3;
+    a.scale = scale;
+    a.softcap = softcap;
+    // Sequences are cut to 2^30 tokens (batch_view), which a longer window never
+    // leaves; the kernels' differences with it then stay within an int.
+    a.window = window < (1 << 30) ? window : 0;
+    return launched(mxfp4::launch_attention(a, cache_view(*cache), batch_view(*batch, cache->page_size), caps.num_sms,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -177,41 +220,16 @@ int mxfp4_attention(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv
                     const mxfp4_kv_batch_t* batch, float scale, float softcap, int window,
                     const uint64_t* tree_mask, void* out, float* lse, void* workspace, size_t workspace_bytes,
                     void* stream) {
-    if (!q || !out || q_heads <= 0 || window < 0 || !(softcap >= 0.f) || std::isinf(softcap) || !std::isfinite(scale))
-        return MXFP4_ERR_INVALID_ARG;
-    if (int rc = cache_status(cache)) return rc;
-    if (int rc = batch_status(batch)) return rc;
-    // The kernels count a request's rows, rounded up to a row tile, in an int.
-    if (q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads || (tree_mask && batch->max_q > 64) ||
-        static_cast<int64_t>(batch->tokens) * (q_heads / cache->kv_heads) > (int64_t(1) << 31) - 256)
-        return MXFP4_ERR_SHAPE;
-    if (q_stride < static_cast<int64_t>(q_heads) * cache->head_dim) return MXFP4_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8))
-        return MXFP4_ERR_ALIGN;
-    if (!workspace) return MXFP4_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return MXFP4_ERR_ALIGN;
-    if (workspace_bytes < mxfp4_attention_workspace_size(q_heads, cache, batch)) return MXFP4_ERR_WORKSPACE;
-    mxfp4::DeviceCaps caps;
-    if (int rc = caps_of(&caps)) return rc;
-    mxfp4::AttentionArgs a{};
-    a.q = q;
-    a.q_stride = q_stride;
-    a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
-    a.out = out;
-    a.lse = lse;
-    a.workspace = workspace;
-    a.status = caps.status;
-    a.q_heads = q_heads;
-    a.max_q = batch->max_q;
-    a.max_seq = batch->max_seq;
-    a.e4m3 = cache->dtype == MXFP4_KV_E4M3;
-    a.scale = scale;
-    a.softcap = softcap;
-    // Sequences are cut to 2^30 tokens (batch_view), which a longer window never
-    // leaves; the kernels' differences with it then stay within an int.
-    a.window = window < (1 << 30) ? window : 0;
-    return launched(mxfp4::launch_attention(a, cache_view(*cache), batch_view(*batch, cache->page_size), caps.num_sms,
-                                            static_cast<cudaStream_t>(stream)));
+    return attention(q, q_stride, q_heads, cache, batch, scale, softcap, window, tree_mask, nullptr, out, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+int mxfp4_attention_at(const void* q, int64_t q_stride, int q_heads, const mxfp4_kv_cache_t* cache,
+                       const mxfp4_kv_batch_t* batch, float scale, float softcap, int window,
+                       const uint64_t* tree_mask, const int32_t* positions, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return attention(q, q_stride, q_heads, cache, batch, scale, softcap, window, tree_mask, positions, out, lse,
+                     workspace, workspace_bytes, stream);
 }
 
 size_t mxfp4_cache_workspace_size(int64_t sequences, int64_t num_pages) {

@@ -37,6 +37,7 @@ struct AttentionArgs {
     const void* q;  // bf16 rows of q_heads * head_dim, q_stride elements apart
     int64_t q_stride;
     const unsigned long long* tree_mask;
+    const int* positions;  // null: a window counts cache indices
     void* out;   // bf16 [tokens, q_heads, head_dim]
     float* lse;  // null or [tokens, q_heads]
     void* workspace;

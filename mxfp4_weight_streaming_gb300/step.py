@@ -317,10 +317,12 @@ def _attention_workspace(stream, q_heads, cache, batch):
 
 
 def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None, out=None, lse=None, workspace=None,
-              stream=None):
+              stream=None, positions=None):
     """bf16 [tokens, q_heads, head_dim]: attention of q (same shape, rows may
     be strided) over the cache. scale defaults to head_dim ** -0.5; tree_mask
-    int64 [tokens] (bit j: sees new token j); lse: float32 [tokens, q_heads] output."""
+    int64 [tokens] (bit j: sees new token j); lse: float32 [tokens, q_heads] output.
+    A window counts cache indices, or with a tree_mask the drafts' positions
+    (int32 [tokens], as rope_append takes them)."""
     tokens, heads, d = shape = q.shape
     if q.dtype is not _BF16 or tokens != batch.tokens or d != cache.head_dim or not q.is_cuda:
         raise ValueError("q: bf16 CUDA tensor [tokens, q_heads, head_dim] expected")
@@ -332,6 +334,9 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
     device = q.get_device()
     if cache.device != device or batch.device != device:
         _elsewhere()
+    if positions is not None:
+        _need(tree_mask is not None, "positions: a tree_mask expected too")
+        _ints(positions, tokens, "positions", device)
     _on_device(device, tree_mask, out, lse, workspace)
     if out is None:
         o = _made(stream, shape, _BF16, q.device)
@@ -344,10 +349,16 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
               "lse: contiguous float32 [tokens, q_heads] expected")
     ws = _attention_workspace(stream, heads, cache, batch) if workspace is None else workspace
     raw = _raw_stream(device) if stream is None else _stream_of(stream, out, lse, workspace)
-    rc = (_L or _lib()).mxfp4_attention(
-        q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
-        d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), o.data_ptr(), _ptr(lse),
-        ws.data_ptr(), ws.nbytes, raw)
+    if positions is None:
+        rc = (_L or _lib()).mxfp4_attention(
+            q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
+            d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), o.data_ptr(), _ptr(lse),
+            ws.data_ptr(), ws.nbytes, raw)
+    else:
+        rc = (_L or _lib()).mxfp4_attention_at(
+            q.data_ptr(), stride if tokens > 1 else heads * d, heads, cache.ref, batch.ref,
+            d ** -0.5 if scale is None else scale, softcap, window, _ptr(tree_mask), positions.data_ptr(),
+            o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, raw)
     if rc:
         _fail(rc, "mxfp4_attention")
     return o

@@ -121,3 +121,54 @@ def test_bounds_far_above_the_lengths():
     a, b = mx.attention(q, pg.cache(mx), tight), mx.attention(q, pg.cache(mx), loose)
     # Two kernels: each off by what attention_bound allows, 2^-7 + 2^-12 of the largest |v| (below 6) at most.
     assert (a.double() - b.double()).abs().max() < 2 * (2 ** -7 + 2 ** -12) * 6
+
+
+# ------------------------------------------------- windows of a tree's drafts
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("window", [1, 5, 70, 130, 4000])
+@pytest.mark.parametrize("heads,kv,dim", [(1, 1, 128), (2, 2, 64), (8, 1, 128), (16, 1, 64)])
+def test_window_counts_from_a_drafts_position(heads, kv, dim, window, dtype):
+    """A draft of depth d sees the keys before the step that decoding it after its ancestors alone would see; which
+    new tokens it sees is the mask's, also where the window is shorter than the path."""
+    mx = lib()
+    news, lens = [16, 40, 3, 1, 7], [700, 171, 3, 90, 9]
+    pg = Paged(window + heads, lens, kv, dim, 16, dtype)
+    g = torch.Generator().manual_seed(window)
+    words, depths = [], []
+    for n in news:
+        m, d = [], []
+        for j in range(n):
+            parent = int(torch.randint(max(0, j - 4), j, (1,), generator=g)) if j else None
+            m.append((m[parent] if j else 0) | 1 << j)
+            d.append(d[parent] + 1 if j else 0)
+        words += m
+        depths += d
+    words[20] = 0
+    t = sum(news)
+    q = randn(gen(window), t, heads, dim)
+    batch = pg.batch(mx, news)
+    first = [seq - n for seq, n in zip(lens, news) for _ in range(n)]
+    positions = ints([f + d for f, d in zip(first, depths)])
+    tree = torch.tensor(words, dtype=torch.int64, device="cuda")
+    out = mx.attention(q, pg.cache(mx), batch, window=window, tree_mask=tree, positions=positions)
+    ref = torch.zeros(t, heads, dim, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    for b, n in enumerate(news):
+        for i in range(n):
+            row, start = pg.start[b] + i, lens[b] - n
+            see = torch.zeros(lens[b], dtype=torch.bool, device="cuda")
+            see[max(0, start + depths[row] - window + 1):start] = True
+            for j in range(n):
+                see[start + j] = bool(words[row] >> j & 1)
+            if not see.any():
+                continue
+            k, v = (x[b][see].repeat_interleave(heads // kv, 1) for x in (pg.k, pg.v))
+            p = torch.softmax(torch.einsum("hd,jhd->hj", q[row].double(), k) * dim ** -0.5, 1)
+            ref[row] = torch.einsum("hj,jhd->hd", p, v)
+            mag[row] = torch.einsum("hj,jhd->hd", p, v.abs())
+    check(out, ref, attention_bound(ref, mag, dtype), f"window {window}")
+    # Positions beyond the request's new tokens count as the nearest of them.
+    high = mx.attention(q, pg.cache(mx), batch, window=window, tree_mask=tree, positions=positions + 10 ** 6)
+    last = ints([f + n - 1 for f, n in zip(first, (n for n in news for _ in range(n)))])
+    same = mx.attention(q, pg.cache(mx), batch, window=window, tree_mask=tree, positions=last)
+    assert torch.equal(high.view(torch.int16), same.view(torch.int16))

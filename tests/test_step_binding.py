@@ -255,6 +255,19 @@ def test_a_table_of_one_column_and_a_gate_of_one_element():
     f(**a)
 
 
+# ----------------------------------------------------------------- positions
+def test_positions_of_drafts(library):
+    f, a = attention_call(positions=ints(4))
+    f(**a)
+    assert library.calls[-1][0] == "mxfp4_attention_at"
+    for bad in (dict(tree_mask=None), dict(positions=ints(5)), dict(positions=ints(4, device=-1))):
+        library.calls.clear()
+        f, a = attention_call(**dict(dict(positions=ints(4)), **bad))
+        with pytest.raises(ValueError):
+            f(**a)
+        assert not library.calls
+
+
 # ------------------------------------------------------------- rotary ramp
 @pytest.mark.parametrize("dim,base,trained,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 4096, 8.0), (64, 1e4, 32768, 4.0),
                                                      (128, 5e5, 8192, 16.0), (32, 1e4, 10 ** 6, 2.0)])

@@ -30,3 +30,16 @@ def test_rows_of_a_kv_head_stay_below_31_bits():
     assert attention((1 << 24) - 1, 256, 2) == mx.MXFP4_ERR_SHAPE  # no room for a row tile's rounding up
     assert attention((1 << 24) - 2, 256, 2, ws=None) == mx.MXFP4_ERR_WORKSPACE  # the next check
     assert attention(1 << 24, 254, 2, ws=None) == mx.MXFP4_ERR_WORKSPACE
+
+
+def test_positions_need_a_tree():
+    cache = KVCacheStruct(k=P, v=P, num_pages=8, layers=1, kv_heads=2, page_size=16, head_dim=64)
+    batch = KVBatchStruct(q_start=P, seq_lens=P, block_table=P, table_width=4, batch=2, tokens=4, max_q=3, max_seq=60)
+
+    def at(tree, positions, ws=P):
+        return mx.load().mxfp4_attention_at(P, 512, 8, ctypes.byref(cache), ctypes.byref(batch), 0.1, 0.0, 8, tree, positions,
+                                            P, None, ws, 1 << 40, None)
+
+    assert at(None, P) == mx.MXFP4_ERR_INVALID_ARG
+    assert at(P, P + 2) == mx.MXFP4_ERR_ALIGN
+    assert at(P, P, ws=None) == at(P, None, ws=None) == at(None, None, ws=None) == mx.MXFP4_ERR_WORKSPACE
