@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             mbar_init(smem_addr(&sh.raw_empty[i]), 128);
         }
         mbar_init(smem_addr(&sh.patch), 1);
-        mbar_init(smem_addr(&sh.q_empty), E4M3 ? 9 : 1);  // the last product; E4M3: the softmax warps too
+        mbar_init(smem_addr(&sh.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&sh.q_full[s]), E4M3 ? 128 : 288);
             mbar_init(smem_addr(&sh.s_full[s]), 1);
@@ -825,18 +825,15 @@ __global__ void __launch_bounds__(tc_threads(E4M3), 1)
             const int n_all = g.steps, n_my = SPLIT ? (n_all + 1 - wg) / 2 : n_all;
             float mul = p.map.mul;
             // q_full alternates between two barriers: q of the segment after next
-            // waits for this one's last probabilities, so no warp with tiles can
-            // still be here when its barrier's phase comes round again. (On one
-            // barrier the next segment's q did that, from the moment this one's
-            // last scores were taken.) The count in q_empty keeps q of the next
-            // segment from being converted while these warps still write out the
-            // last one's results: 256 requests x 8 tokens over 300 190 us against
-            // 205, 64 x 8 over 4,090 235 against 238.
-            if constexpr (E4M3) {
+            // waits for this one's last probabilities, so no group with tiles can
+            // still be here when its barrier's phase comes round again (on one
+            // barrier the next segment's q would do that, from the moment this
+            // one's last scores are taken). A group without tiles has no use for
+            // it. A count of these warps in q_empty instead measured the same or
+            // slower (256 requests x 8 tokens over 300: 205 us against 194).
+            if (E4M3 && n_my) {
                 if (!wait_all(sh.q_full[(turn_seg - 1) & 1], ((turn_seg - 1) >> 1) & 1)) break;
                 const int e = sh.q_exp[(turn_seg - 1) & 1][(SPLIT ? 0 : wg * 128) + r];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
                 const float ks = p.cache.k_scale ? p.cache.k_scale[g.head] : 1.f;
                 mul = fmaxf(fabsf(mul * ks * __uint_as_float(static_cast<uint32_t>(127 + e) << 23)), 1e-36f);
             }
