@@ -643,9 +643,8 @@ cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
 
 template <int D, bool PLACED>
 cudaError_t launch_d(const Params& p, bool e4m3, int mt, int ctas, cudaStream_t stream) {
-    if (mt == 1)
-        return e4m3 ? launch<D, true, 1, PLACED>(p, ctas, stream) : launch<D, false, 1, PLACED>(p, ctas, stream);
-    return e4m3 ? launch<D, true, 2, PLACED>(p, ctas, stream) : launch<D, false, 2, PLACED>(p, ctas, stream);
+    if (!e4m3) return launch<D, false, 1, PLACED>(p, ctas, stream);  // more than 16 rows: attention_tc.cu
+    return mt == 1 ? launch<D, true, 1, PLACED>(p, ctas, stream) : launch<D, true, 2, PLACED>(p, ctas, stream);
 }
 
 // The tensor-core kernel where the rows of a KV head fill enough of its
