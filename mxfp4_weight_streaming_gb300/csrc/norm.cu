@@ -215,8 +215,14 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, int num_sms, cudaStr
     for (const void* q : ptrs) vec = vec && reinterpret_cast<uintptr_t>(q) % 16 == 0;
     p.tokens = static_cast<int>(a.tokens);
     const int chunks = static_cast<int>((a.n + 7) / 8);  // 8-value chunks of a row
+    // Blocks per SM: as many as the registers of 1,024 threads allow at once, so
+    // that every block has rows to the end (us; rms, post weight, no gate):
+    // 32,768 rows of 1,024: 8 blocks 49.5, 4 68, 12 57; 16,384 of 2,048: 4 52, 6
+    // 60; 8,192 of 4,096: 4 46, 2 56, 3 57; 4,096 of 7,168: 2 46, 1 57. Beyond
+    // 16,384 columns a row's values spill: 2,048 rows of 18,432 take 193 us, 23 %
+    // of the copy rate.
     if (chunks <= 128) return launch<128, 1>(p, 8, num_sms, vec, a.layer, stream);
-    if (chunks <= 256) return launch<256, 1>(p, 6, num_sms, vec, a.layer, stream);
+    if (chunks <= 256) return launch<256, 1>(p, 4, num_sms, vec, a.layer, stream);
     if (chunks <= 512) return launch<256, 2>(p, 4, num_sms, vec, a.layer, stream);
     if (chunks <= 1024) return launch<512, 2>(p, 2, num_sms, vec, a.layer, stream);
     if (chunks <= 2048) return launch<1024, 2>(p, 1, num_sms, vec, a.layer, stream);
