@@ -648,10 +648,12 @@ cudaError_t launch_d(const Params& p, bool e4m3, int mt, int ctas, cudaStream_t 
 }
 
 // The tensor-core kernel where the rows of a KV head fill enough of its
-// 128-row tiles. bf16, groups of 7, 64 requests of 4,090 tokens (us, this
-// kernel / attention_tc.cu): 7 rows 172 / 183, 14 rows 173 / 185; 28 rows over
-// one request of 131,069 tokens 130 / 99. E4M3, 28 rows: 221 / 269 (there the
-// bytes have to pass through converting warps).
+// 128-row tiles (us, this kernel / attention_tc.cu). bf16, groups of 7, D = 128,
+// 64 requests of 4,090 tokens: 7 rows 173 / 185, 14 rows 175 / 187; 28 rows over
+// one request of 131,069 tokens 130 / 99. E4M3, where the bytes have to pass
+// through converting warps: 14 rows 102 / 225; 28 rows 216 / 228, 8 requests of
+// 2,000 34 / 36, 16 of 1,000 (21 rows) 34 / 37, but one of 131,069 116 / 102;
+// D = 64, 20 rows: 64 x 4,090 150 / 138, 8 x 2,000 22 / 23, one of 131,069 82 / 73.
 bool use_tc(int64_t rows, bool e4m3) { return rows > (e4m3 ? 32 : 16); }
 
 template <int D, bool E4M3>
