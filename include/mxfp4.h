@@ -393,8 +393,9 @@ int mxfp4_residual_norm(const void* x, const void* residual, int64_t tokens, int
  * of each q and k head turn in pairs by position * inv_freq[j]: pair j is
  * the elements (2j, 2j+1) (interleaved != 0) or (j, j + rotary_dim/2):
  *   (a, b) -> (a cos - b sin, a sin + b cos) * factor
- * The rest of the head, and V, pass unchanged. Angles are reduced in fp64,
- * so long positions keep their accuracy. Stretching a model to longer
+ * The rest of the head, and V, pass unchanged. Angles are reduced as sums of
+ * two fp32 numbers, so long positions keep their accuracy: off by 2^-22 +
+ * |position| * inv_freq * 2^-47 of a turn at most. Stretching a model to longer
  * contexts is a matter of inv_freq and factor.
  *   qkv          device bf16, rows of (q_heads + 2 kv_heads) * head_dim (q,
  *                then k, then v) qkv_stride elements apart, 16-byte aligned,

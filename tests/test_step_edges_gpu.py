@@ -1,10 +1,12 @@
 """The step's norms, rotary positions and page bookkeeping where calls go to
 their limits."""
+import math
+
 import pytest
 import torch
 
 from gpu_cases import lib
-from step_cases import E4M3, Paged, gen, ints, randn
+from step_cases import E4M3, Paged, check, gen, ints, randn
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -109,3 +111,25 @@ def test_e4m3_rows_are_divided_by_their_scale():
     want = (x.float()[None] / scales[:, None, None]).clamp(-448, 448).to(E4M3)  # [heads, 4, 128]
     for got in (pool, vpool):
         assert torch.equal(got.view(torch.uint8)[1, :, :4], want.view(torch.uint8))
+
+
+# ------------------------------------------------------------ long positions
+@pytest.mark.parametrize("near", [0, 2 ** 17, 2 ** 24, 2 ** 28, 2 ** 31 - 70])
+def test_angles_at_long_positions(near):
+    """Error of an angle: 2^-22 of a turn up to position 2^24, and 2^-47 of position * inv_freq beyond."""
+    mx = lib()
+    pos = [near + 7 * i for i in range(9)] + [-(near + 5 * i) for i in range(9)]
+    inv, _ = mx.rope_frequencies(128)
+    inv[0] = 0.9999999  # products that are not whole
+    pg = Paged(1, [18], 1, 128, 32)
+    qkv = torch.ones(18, 4 * 128, dtype=BF16, device="cuda")
+    q = mx.rope_append(qkv, 2, inv, pg.cache(mx), pg.batch(mx, [18]), positions=ints(pos))
+    p64 = torch.tensor(pos, dtype=torch.float64, device="cuda")
+    ang = p64[:, None] * inv.double()
+    c, s = torch.cos(ang), torch.sin(ang)
+    ref = torch.cat([c - s, s + c], 1)
+    turns = 2 ** -22 + (p64.abs()[:, None] * inv.double() * 2 ** -47)
+    # An angle off by t turns moves cos - sin by at most sqrt(2) 2 pi t; sines are good to 2^-21; one bf16 rounding.
+    slack = (turns * 2 * math.pi * math.sqrt(2) + 2 ** -20).repeat(1, 2)
+    for h in range(2):
+        check(q[:, h], ref, ref.abs() * 2 ** -8 + slack, f"positions near {near}")
