@@ -316,7 +316,9 @@ int mxfp4_moe_noalloc(const void* x, int64_t t, int64_t hidden, const float* rou
  * calls above: their bf16 inputs and outputs are mxfp4_linear's outputs and
  * inputs. No call synchronises, and every length and page number is read on
  * the device, so a step can be captured once in a CUDA graph and replayed
- * while the lengths change.
+ * while the lengths change. (mxfp4_cache_update writes the new table and
+ * lengths beside the old ones: a captured step copies them to where its other
+ * calls read them.)
  *
  * Paged KV cache. K and V each live in a pool of pages of page_size tokens;
  * a page holds [kv_heads][page_size][head_dim] elements, dense, and pages

@@ -378,7 +378,8 @@ def cache_update(cache, block_table, seq_lens, parent, keep, grow, workspace=Non
     parent[i] (negative: begins empty), cut to keep[i] tokens (keep None:
     all), with room for grow[i] more. Returns (block_table, seq_lens, copies,
     info): int32 [n, width], [n], [n, 3] for cache_copy, and [pages left
-    free, pages asked for in vain]."""
+    free, pages asked for in vain]. A step captured in a CUDA graph copies
+    table and lengths to the tensors of its KVBatch."""
     n, old, device = parent.numel(), seq_lens.numel(), block_table.get_device()
     _ints(parent, n, "parent", device)
     _ints(grow, n, "grow", device)

@@ -133,3 +133,76 @@ def test_angles_at_long_positions(near):
     slack = (turns * 2 * math.pi * math.sqrt(2) + 2 ** -20).repeat(1, 2)
     for h in range(2):
         check(q[:, h], ref, ref.abs() * 2 ** -8 + slack, f"positions near {near}")
+
+
+# ------------------------------------------------------------- a whole step
+def test_a_step_captured_once():
+    """Room for the new tokens, their page copies, norm, rotary positions with the cache write, attention and accept
+    in one graph: replays while lengths, pages and accepted counts change give what the calls give one by one."""
+    mx = lib()
+    heads, kv, dim, page, new, n, width = 4, 2, 64, 16, 4, 3, 12
+    hidden, qkv_width = heads * dim, (heads + 2 * kv) * dim
+    inv, factor = mx.rope_frequencies(dim)
+    same, grow = ints(list(range(n))), ints([new] * n)
+    start = ints([i * new for i in range(n + 1)])
+
+    class Step:
+        def __init__(self):
+            g = gen(5)
+            pool = torch.zeros(2, 2, 60, kv, page, dim, dtype=BF16, device="cuda")  # K and V, two layers
+            self.cache, self.pool = mx.KVCache(pool[0], pool[1]), pool
+            self.layers = [self.cache.layer(i) for i in range(2)]
+            self.table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+            self.lens, self.keep = ints([0] * n), ints([0] * n)
+            self.x, self.res, self.w = randn(g, n * new, hidden), randn(g, n * new, hidden), randn(g, hidden)
+            self.qkv = randn(g, n * new, qkv_width)
+            self.path, self.took = torch.zeros(n, new, dtype=torch.int32, device="cuda"), ints([1] * n)
+            # The table and lengths that calls read: every step's new ones are copied there.
+            self.batch = mx.KVBatch(start, self.lens, self.table, tokens=n * new, max_q=new, max_seq=width * page)
+
+        def run(self):
+            table, lens, copies, self.info = mx.cache_update(self.cache, self.table, self.lens, same, self.keep, grow)
+            mx.cache_copy(self.cache, copies)
+            self.table.copy_(table)
+            self.lens.copy_(lens)
+            r = self.res
+            for layer in self.layers:
+                y, r = mx.residual_norm(self.x, r, self.w)
+                q = mx.rope_append(self.qkv, heads, inv, layer, self.batch, factor=factor)
+                a = mx.attention(q, layer, self.batch)
+                r = a.view(n * new, hidden) + y
+            self.out = r
+            self.keep.copy_(mx.cache_accept(self.cache, self.batch, self.path, self.took))
+
+    plain, caught = Step(), Step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        caught.run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caught.run()
+    for s in (caught,):  # as at the start
+        s.table.fill_(-1)
+        s.lens.zero_()
+        s.keep.zero_()
+        s.pool.zero_()
+    for turn in range(9):
+        g = gen(100 + turn)
+        fresh = randn(g, n * new, qkv_width), randn(g, n * new, hidden)
+        order = torch.rand(n, new, generator=g, device="cuda").argsort(1).to(torch.int32)
+        took = torch.randint(1, new + 1, (n,), generator=g, device="cuda").to(torch.int32)
+        for s in (plain, caught):
+            s.qkv.copy_(fresh[0])
+            s.x.copy_(fresh[1])
+            s.path.copy_(order)
+            s.took.copy_(took)
+        plain.run()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("table", "lens", "keep", "info", "out", "pool"):
+            a, b = getattr(plain, name), getattr(caught, name)
+            assert torch.equal(a, b), f"step {turn}: {name}"
+        assert plain.info[1].item() == 0 and torch.isfinite(plain.out.float()).all()
+    assert int(plain.keep.min()) >= 9
