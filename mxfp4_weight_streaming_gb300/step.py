@@ -274,7 +274,8 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
                 stream=None):
     """Turns q and k of the rows of qkv (bf16 [tokens, (q_heads + 2 kv_heads) *
     head_dim], q then k then v) by their positions, writes k and v to the
-    cache and returns q, bf16 [tokens, q_heads, head_dim]. inv_freq float32
+    cache and returns q, bf16 [tokens, q_heads, head_dim] (rows of no request
+    are left as they are, uninitialised without out=). inv_freq float32
     [rotary_dim / 2] (None: only the cache write)."""
     tokens, d = batch.tokens, cache.head_dim
     if qkv.dtype is not _BF16 or qkv.shape != (tokens, (q_heads + 2 * cache.kv_heads) * d) or not qkv.is_cuda or \
@@ -299,7 +300,7 @@ def rope_append(qkv, q_heads, inv_freq, cache, batch, interleaved=False, positio
         q = out
     raw = _raw_stream(device) if stream is None else _stream_of(stream, out)
     rc = (_L or _lib()).mxfp4_rope_append(
-        qkv.data_ptr(), qkv.stride(0), q_heads, _ptr(positions), _ptr(inv_freq), rotary, interleaved, factor,
+        qkv.data_ptr(), qkv.stride(0) if tokens > 1 else qkv.shape[1], q_heads, _ptr(positions), _ptr(inv_freq), rotary, interleaved, factor,
         cache.ref, batch.ref, q.data_ptr(), raw)
     if rc:
         _fail(rc, "mxfp4_rope_append")
@@ -319,7 +320,7 @@ def _attention_workspace(stream, q_heads, cache, batch):
 def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None, out=None, lse=None, workspace=None,
               stream=None, positions=None):
     """bf16 [tokens, q_heads, head_dim]: attention of q (same shape, rows may
-    be strided) over the cache. scale defaults to head_dim ** -0.5; tree_mask
+    be strided) over the cache; rows of no request are left as they are. scale defaults to head_dim ** -0.5; tree_mask
     int64 [tokens] (bit j: sees new token j); lse: float32 [tokens, q_heads] output.
     A window counts cache indices, or with a tree_mask the drafts' positions
     (int32 [tokens], as rope_append takes them)."""

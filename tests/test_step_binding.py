@@ -191,6 +191,18 @@ def test_handles_over_two_devices_are_refused():
             mx.KVBatch(*args, tokens=4, max_q=2, max_seq=60)
 
 
+def test_the_row_stride_of_a_single_token_does_not_matter(library):
+    batch = mx.KVBatch(ints(2), ints(1), ints(1, 4), tokens=1, max_q=1, max_seq=60)
+    row = torch.zeros(8 * 64, dtype=BF16).as_strided((1, 8 * 64), (3, 1))
+    f, a = rope_call(qkv=OnGpu(row), batch=batch, positions=None, out=bf16(1, 4, 64))
+    f(**a)
+    assert library.calls[-1][1][1] == 8 * 64
+    q = torch.zeros(4 * 64, dtype=BF16).as_strided((1, 4, 64), (3, 64, 1))
+    f, a = attention_call(q=OnGpu(q), batch=batch, tree_mask=None, out=bf16(1, 4, 64), lse=None)
+    f(**a)
+    assert library.calls[-1][1][1] == 4 * 64
+
+
 # ------------------------------------------------------------------- streams
 class Stream:
     cuda_stream = 77
