@@ -21,6 +21,7 @@ KV_BF16, KV_E4M3 = 0, 1
 
 _BF16, _E4M3, _F32, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
 _empty = torch.empty
+_MOST = 2 ** 31 - 1  # ctypes takes a larger number by its low bits
 _L = None  # the loaded library, from the first call on
 
 
@@ -185,7 +186,7 @@ class KVBatch:
               and block_table.shape[0] == b and _strides(block_table)[1] in (1, None),
               "block_table: int32 CUDA tensor [batch, width] expected")
         self.q_start, self.seq_lens, self.block_table = q_start, seq_lens, block_table
-        self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), int(max_q), int(max_seq)
+        self.batch, self.tokens, self.max_q, self.max_seq = b, int(tokens), min(int(max_q), _MOST), min(int(max_seq), _MOST)
         width = block_table.shape[1]
         stride = _row_stride(block_table)
         self.struct = KVBatchStruct(_ptr(q_start), _ptr(seq_lens), _ptr(block_table), stride, width, b, self.tokens,
@@ -349,6 +350,8 @@ def attention(q, cache, batch, scale=None, softcap=0.0, window=0, tree_mask=None
         _need(lse.dtype is _F32 and lse.shape == shape[:2] and lse.is_contiguous(),
               "lse: contiguous float32 [tokens, q_heads] expected")
     ws = _attention_workspace(stream, heads, cache, batch) if workspace is None else workspace
+    if window > _MOST:
+        window = _MOST
     raw = _raw_stream(device) if stream is None else _stream_of(stream, out, lse, workspace)
     if positions is None:
         rc = (_L or _lib()).mxfp4_attention(

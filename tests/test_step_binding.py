@@ -203,6 +203,14 @@ def test_the_row_stride_of_a_single_token_does_not_matter(library):
     assert library.calls[-1][1][1] == 4 * 64
 
 
+def test_numbers_beyond_32_bits_are_cut_not_wrapped(library):
+    f, a = attention_call(window=2 ** 32 + 5)
+    f(**a)
+    assert library.calls[-1][1][7] == 2 ** 31 - 1
+    loose = mx.KVBatch(ints(3), ints(2), ints(2, 4), tokens=4, max_q=2 ** 32 + 1, max_seq=2 ** 40)
+    assert (loose.struct.max_q, loose.struct.max_seq) == (2 ** 31 - 1, 2 ** 31 - 1)
+
+
 # ------------------------------------------------------------------- streams
 class Stream:
     cuda_stream = 77
