@@ -10,7 +10,8 @@
 // joined once per item. Scores and outputs are mma.sync m16n8k16 with fp32
 // accumulation: at up to 32 rows the products take less time than the bytes.
 //
-// bf16 cache: bf16 products, probabilities rounded to bf16. E4M3 cache: the
+// bf16 cache: bf16 products, probabilities rounded to bf16 (a product takes
+// both operands in one type; attention_tc.cu has the errors). E4M3 cache: the
 // rows become f16 in registers (exact), q is scaled per row by a power of
 // two into f16's range and probabilities are f16. Sums, maxima and
 // accumulators are fp32.

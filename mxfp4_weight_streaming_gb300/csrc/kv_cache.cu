@@ -6,7 +6,9 @@
 // barriers cost less than more launches would. Copy and accept move
 // contiguous 16-byte vectors, a block per page or request, head and K or V of
 // a layer. Update and copy of 32 beams in 24 layers (93 MB moved each way) take
-// 21 us together, accept and update of 8 requests in 16 layers 13 us.
+// 21 us together, accept and update of 8 requests in 16 layers 13 us. Update
+// alone: 5 us with a pool of 654 pages, 21 with 16,384, 72 with 65,536 (its two
+// passes over the pool).
 #include <climits>
 
 #include "step_launch.h"
