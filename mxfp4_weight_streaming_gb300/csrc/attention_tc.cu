@@ -29,8 +29,9 @@
 // type too, since a product takes both operands in one type: each is off by up
 // to 2^-8 (2^-11) of itself, the outputs by 2.0e-3 to 2.4e-3 in the rms against
 // 1.7e-3 by their own rounding to bf16; with f16 it does not show (but ones
-// below 2^-25 of the largest are 0 there). Their sum is of the unrounded ones. Elements of q below 2^-17 of their row's largest lose
-// bits in f16, 2^-25 of the largest at most: as little as the scores' fp32 sums.
+// below 2^-25 of the largest are 0 there). Their sum is of the unrounded ones.
+// Elements of q below 2^-17 of their row's largest lose bits in f16, 2^-25 of
+// the largest at most: as little as the scores' fp32 sums.
 //
 // A row's running maximum is raised only when a score exceeds it by 2^8, so
 // O is seldom rescaled (by the row's own thread, after the stream's last
