@@ -513,6 +513,79 @@ int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* ba
                        int path_len, const int32_t* n_accept, int32_t* lens_out, void* stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Many tokens at once (the chunks of a prompt, large batches): activations as
+ * microscaled (MX) codes, and their products with MXFP4 weights on the tensor
+ * cores. A block's chain is norm -> codes -> product -> codes -> product.
+ *
+ * MX codes of rows of k values (k % 32 == 0): each 32 consecutive values of a
+ * row share one E8M0 byte s, a value is its element times 2^(s-127).
+ *   codes   E4M3: uint8 [t, k];  E2M1: uint8 [t, k/2], the even index in the
+ *           low nibble (as in the weights)
+ *   scales  uint8 [t, k/32]
+ * The scale is the smallest power of two, 2^-127 at least, that keeps every
+ * element of the block within its type (448 or 6): nothing saturates. Elements
+ * are rounded to nearest, ties to even. A block that holds a NaN or an
+ * infinity gets scale 255, NaN, and every output it takes part in is NaN.
+ * (mxfp4_quantize's rule for weights is another: theirs may saturate.)
+ */
+typedef enum {
+    MXFP4_MX_E4M3 = 0, /* 8 bits: 4 significant ones, 8.25 bits a value in all */
+    MXFP4_MX_E2M1 = 1  /* 4 bits: 2 significant ones, 4.25 bits a value */
+} mxfp4_mx_format;
+
+/*
+ * Rows of bf16 as MX codes; swiglu != 0: of z[j] = SiLU(x[j]) * x[k + j] (fp32).
+ *   x       device bf16, t rows of k (swiglu: 2 k) values, x_stride elements
+ *           apart (0: dense), 16-byte aligned, x_stride % 8 == 0
+ *   xq, xs  device codes (16-byte aligned) and scales (outputs)
+ */
+int mxfp4_quantize_mx(const void* x, int64_t x_stride, int64_t t, int64_t k, int swiglu, int format, void* xq,
+                      uint8_t* xs, void* stream);
+
+/*
+ * mxfp4_residual_norm with y as MX codes of the unrounded fp32 values.
+ *   n       a multiple of 32, at most 32768; every pointer but ys 16-byte
+ *           aligned, gate_stride % 8 == 0
+ *   yq, ys  device codes and scales of y (outputs)
+ * Every other argument is as there; r_out may be residual.
+ */
+int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, int64_t n, const void* post_weight,
+                           const void* post_bias, const void* gate, int64_t gate_stride, float scale,
+                           const void* weight, const void* bias, float weight_offset, float eps, int layer, int format,
+                           void* yq, uint8_t* ys, void* r_out, void* stream);
+
+/*
+ * y[i][j] = bf16( sum_k x[i][k] * w[j][k] ) for any number of tokens.
+ *   xq, xs  device MX codes and scales of x [t, k], 16-byte aligned; format:
+ *           theirs
+ *   k       a multiple of 128
+ *   wq, ws  device uint8 [n, k/2], [n, k/32], MXFP4 weights as for
+ *           mxfp4_linear (scale bytes up to 254), 16-byte aligned (wq with
+ *           E4M3 activations: 32)
+ *   y       device bf16 [t, n], 2-byte aligned (output; 16-byte aligned with
+ *           n % 8 == 0 takes the wide stores)
+ * Products of codes are exact, sums fp32 in the tensor cores' order. Codes and
+ * scales that mxfp4_residual_norm_mx or mxfp4_swiglu_mx writes are meant as
+ * activations.
+ */
+int mxfp4_linear_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq,
+                    const uint8_t* ws, int64_t n, void* y, void* stream);
+
+/*
+ * The gated half of an FFN, from codes to codes:
+ *   h[i][j] = SiLU( sum_k x[i][k] w1[j][k] ) * sum_k x[i][k] w1[inter + j][k]
+ * in fp32, and its MX codes (out_format), with no intermediate in memory.
+ *   w1q, w1s  device uint8 [2*inter, k/2], [2*inter, k/32] (gate rows first)
+ *   inter     a multiple of 32
+ *   hq, hs    device codes (16-byte aligned) and scales of h [t, inter]
+ *             (outputs)
+ * Every other argument is as for mxfp4_linear_mx.
+ */
+int mxfp4_swiglu_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* w1q,
+                    const uint8_t* w1s, int64_t inter, int out_format, void* hq, uint8_t* hs, void* stream);
+
+/*
  * Synchronizes `stream`, then returns MXFP4_OK, MXFP4_ERR_TIMEOUT if some
  * kernel of this library on the current device gave up a bounded wait since
  * the last call, or MXFP4_ERR_CUDA if the stream reports an error. Clears

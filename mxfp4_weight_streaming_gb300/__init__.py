@@ -15,6 +15,10 @@ attention over the paged KV cache, the cache's pages) is in step.py and
 available from here: KVCache, KVBatch, residual_norm, rope_frequencies,
 rope_append, attention, attention_workspace, cache_update, cache_workspace,
 cache_copy, cache_accept.
+
+Many tokens at once (activations as microscaled codes, and their products with
+MXFP4 weights) are in chunk.py and available from here: quantize_mx,
+residual_norm_mx, linear_mx, swiglu_mx.
 """
 from __future__ import annotations
 
@@ -35,7 +39,8 @@ MXFP4_ERR_TIMEOUT = 6
 EXPORTED = ["mxfp4_strerror", "mxfp4_quantize", "mxfp4_linear", "mxfp4_linear_plan", "mxfp4_moe_workspace_size",
             "mxfp4_moe", "mxfp4_last_device_status", "mxfp4_residual_norm", "mxfp4_rope_append",
             "mxfp4_attention_workspace_size", "mxfp4_attention", "mxfp4_attention_at", "mxfp4_cache_workspace_size",
-            "mxfp4_cache_update", "mxfp4_cache_copy", "mxfp4_cache_accept"]
+            "mxfp4_cache_update", "mxfp4_cache_copy", "mxfp4_cache_accept", "mxfp4_quantize_mx",
+            "mxfp4_residual_norm_mx", "mxfp4_linear_mx", "mxfp4_swiglu_mx"]
 
 _lib = None
 
@@ -106,6 +111,14 @@ def load() -> ctypes.CDLL:
     L.mxfp4_cache_copy.argtypes = [P, P, I, P]
     L.mxfp4_cache_accept.restype = I
     L.mxfp4_cache_accept.argtypes = [P, P, P, I, P, P, P]
+    L.mxfp4_quantize_mx.restype = I
+    L.mxfp4_quantize_mx.argtypes = [P, I64, I64, I64, I, I, P, P, P]
+    L.mxfp4_residual_norm_mx.restype = I
+    L.mxfp4_residual_norm_mx.argtypes = [P, P, I64, I64, P, P, P, I64, F, P, P, F, F, I, I, P, P, P, P]
+    L.mxfp4_linear_mx.restype = I
+    L.mxfp4_linear_mx.argtypes = [P, P, I, I64, I64, P, P, I64, P, P]
+    L.mxfp4_swiglu_mx.restype = I
+    L.mxfp4_swiglu_mx.argtypes = [P, P, I, I64, I64, P, P, I64, I, P, P, P]
     _lib = L
     return L
 
@@ -261,10 +274,16 @@ _STEP = ("KVBatch", "KVCache", "attention", "attention_workspace", "cache_accept
          "cache_workspace", "residual_norm", "rope_append", "rope_frequencies")
 
 
+_CHUNK = ("linear_mx", "quantize_mx", "residual_norm_mx", "swiglu_mx")
+
+
 def __getattr__(name):
-    """step.py needs torch, which the rest of this module imports only when called: it is read at first use."""
-    if name not in _STEP:
+    """step.py and chunk.py need torch, which the rest of this module imports only when called: they are read at first use."""
+    if name in _STEP:
+        from . import step as part
+    elif name in _CHUNK:
+        from . import chunk as part
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import step
-    globals().update((n, getattr(step, n)) for n in _STEP)
+    globals().update((n, getattr(part, n)) for n in (_STEP if name in _STEP else _CHUNK))
     return globals()[name]

@@ -14,6 +14,7 @@
 #include "moe_launch.h"
 #include "tc_linear_launch.h"
 #include "f4_linear_launch.h"
+#include "mx_launch.h"
 #include "step_common.cuh"
 #include "step_launch.h"
 #include "mxfp4.h"
@@ -161,6 +162,28 @@ cudaError_t encode_kv_map(CUtensorMap* map, const void* pool, const CacheView& c
                      {d * e, page * d * e, static_cast<cuuint64_t>(c.page_stride) * e},
                      {e4m3 ? static_cast<cuuint32_t>(d) : 64u, rows, 1, 1},
                      e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t row_bytes, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estride[2] = {1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box,
+                                estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_spread_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t k, int box_rows) {
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(k / 128)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(k / 2), 64};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<uint8_t*>(codes), dims,
+                                strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 int encode_weights(CUtensorMap* map, const uint8_t* wq, int64_t rows, int64_t k, int steps, int* is3d) {

@@ -1,0 +1,116 @@
+// C ABI of a prompt chunk's way through MXFP4 weights: argument checks, then
+// the launches of mx_quantize.cu, mx_product.cu and norm.cu.
+#include "mx_launch.h"
+#include "step_common.cuh"
+#include "step_launch.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA; }
+
+bool known(int format) { return format == MXFP4_MX_E4M3 || format == MXFP4_MX_E2M1; }
+
+constexpr int64_t kMost = int64_t(1) << 31;  // coordinates of a copy are ints
+
+int product(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq, const uint8_t* ws,
+            int64_t n, bool swiglu, int out_format, void* y, uint8_t* ys, void* stream) {
+    if (!xq || !xs || !wq || !ws || !y || (swiglu && !ys) || t <= 0 || k <= 0 || n <= 0 || !known(format) ||
+        !known(out_format))
+        return MXFP4_ERR_INVALID_ARG;
+    if (k % 128 || k >= kMost || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
+        return MXFP4_ERR_SHAPE;
+    for (const void* p : {xq, static_cast<const void*>(xs), static_cast<const void*>(ws)})
+        if (!aligned(p, 16)) return MXFP4_ERR_ALIGN;
+    if (!aligned(wq, format == MXFP4_MX_E4M3 ? 32 : 16) || !aligned(y, swiglu ? 16 : 2)) return MXFP4_ERR_ALIGN;
+    mxfp4::DeviceCaps caps;
+    if (int rc = mxfp4::device_caps(&caps)) return rc;
+    mxfp4::MxProductArgs a{};
+    a.xq = xq;
+    a.xs = xs;
+    a.wq = wq;
+    a.ws = ws;
+    a.t = t;
+    a.k = k;
+    a.n = n;
+    a.y = y;
+    a.ys = ys;
+    a.e2m1 = format == MXFP4_MX_E2M1;
+    a.swiglu = swiglu;
+    a.out_e2m1 = out_format == MXFP4_MX_E2M1;
+    a.status = caps.status;
+    return launched(mxfp4::launch_mx_product(a, caps.num_sms, caps.max_smem, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int mxfp4_quantize_mx(const void* x, int64_t x_stride, int64_t t, int64_t k, int swiglu, int format, void* xq,
+                      uint8_t* xs, void* stream) {
+    if (!x || !xq || !xs || t <= 0 || k <= 0 || !known(format) || (x_stride && x_stride < (swiglu ? 2 : 1) * k))
+        return MXFP4_ERR_INVALID_ARG;
+    if (k % 32 || k >= kMost || t >= kMost) return MXFP4_ERR_SHAPE;
+    if (!aligned(x, 16) || x_stride % 8 || !aligned(xq, 16)) return MXFP4_ERR_ALIGN;
+    mxfp4::DeviceCaps caps;
+    if (int rc = mxfp4::device_caps(&caps)) return rc;
+    mxfp4::MxQuantizeArgs a{};
+    a.x = x;
+    a.x_stride = x_stride ? x_stride : (swiglu ? 2 : 1) * k;
+    a.t = t;
+    a.k = k;
+    a.xq = xq;
+    a.xs = xs;
+    a.swiglu = swiglu != 0;
+    a.e2m1 = format == MXFP4_MX_E2M1;
+    return launched(mxfp4::launch_mx_quantize(a, caps.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, int64_t n, const void* post_weight,
+                           const void* post_bias, const void* gate, int64_t gate_stride, float scale,
+                           const void* weight, const void* bias, float weight_offset, float eps, int layer, int format,
+                           void* yq, uint8_t* ys, void* r_out, void* stream) {
+    if (!x || !residual || !weight || !yq || !ys || !r_out || tokens <= 0 || n <= 0 || (post_bias && !post_weight) ||
+        gate_stride < 0 || (gate_stride && gate_stride < n) || !(eps >= 0.f) || !known(format) || yq == r_out)
+        return MXFP4_ERR_INVALID_ARG;
+    if (n > 32768 || n % 32 || tokens >= kMost) return MXFP4_ERR_SHAPE;
+    for (const void* p : {x, residual, post_weight, post_bias, gate, weight, bias, static_cast<const void*>(yq),
+                          static_cast<const void*>(r_out)})
+        if (!aligned(p, 16)) return MXFP4_ERR_ALIGN;
+    if (gate_stride % 8) return MXFP4_ERR_ALIGN;
+    mxfp4::DeviceCaps caps;
+    if (int rc = mxfp4::device_caps(&caps)) return rc;
+    mxfp4::ResidualNormArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.post_weight = post_weight;
+    a.post_bias = post_bias;
+    a.gate = gate;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = yq;
+    a.ys = ys;
+    a.r_out = r_out;
+    a.tokens = tokens;
+    a.n = n;
+    a.gate_stride = gate_stride;
+    a.scale = scale;
+    a.eps = eps;
+    a.weight_offset = weight_offset;
+    a.layer = layer != 0;
+    a.e2m1 = format == MXFP4_MX_E2M1;
+    return launched(mxfp4::launch_residual_norm(a, caps.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mxfp4_linear_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq,
+                    const uint8_t* ws, int64_t n, void* y, void* stream) {
+    return product(xq, xs, format, t, k, wq, ws, n, false, MXFP4_MX_E4M3, y, nullptr, stream);
+}
+
+int mxfp4_swiglu_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* w1q,
+                    const uint8_t* w1s, int64_t inter, int out_format, void* hq, uint8_t* hs, void* stream) {
+    return product(xq, xs, format, t, k, w1q, w1s, inter, true, out_format, hq, hs, stream);
+}
+
+}  // extern "C"

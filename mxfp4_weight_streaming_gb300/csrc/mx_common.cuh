@@ -1,0 +1,80 @@
+// Microscaled (MX) activations: blocks of 32 values along a row share one E8M0
+// scale 2^(s-127); elements are E4M3 or E2M1 (two codes a byte, the even index
+// in the low nibble). What the kernels that make such blocks share.
+//
+// A block's scale is the smallest power of two that keeps every element within
+// its type: with m = max|z|, the least e >= -127 with m <= 448 * 2^e (6 * 2^e).
+// (The weights' packer takes floor(log2 m) - 2 and lets values saturate, up to
+// 25 % off; an activation's largest values carry most of a product.) Element =
+// nearest (ties to even) of z / 2^e. A block with a NaN or an infinity has scale
+// NaN (255), which makes every product that it takes part in NaN.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_common.cuh"
+
+namespace mxfp4 {
+namespace mx {
+
+constexpr uint32_t kNanScale = 255;
+
+// Scale byte of a block by the bits of its largest magnitude. 448 = 1.75 * 2^8
+// and 6 = 1.5 * 2^2, so the fraction decides between two exponents.
+template <bool E2M1>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return kNanScale;
+    const int e = static_cast<int>(amax_bits >> 23) - (E2M1 ? 2 : 8) +
+                  ((amax_bits & 0x7fffffu) > (E2M1 ? 0x400000u : 0x600000u));
+    return static_cast<uint32_t>(max(e, 0));
+}
+
+// 2^(127 - s): what a block's values are multiplied with (exact).
+__device__ __forceinline__ float inverse_scale(uint32_t s) { return exp2_int(127 - static_cast<int>(s)); }
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// N values, already in units of their scale, as N / 4 words of E4M3 or N / 8 of E2M1.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// N values of one block (its scale byte s) as codes. Under a NaN scale E4M3
+// codes are NaN too; E2M1 has none.
+template <bool E2M1, int N>
+__device__ __forceinline__ void encode(const float* v, uint32_t s, uint32_t (&out)[E2M1 ? N / 8 : N / 4]) {
+    const float f = s == kNanScale ? 0.f : inverse_scale(s);
+    float z[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = v[i] * f;
+    if constexpr (E2M1) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) out[i] = s == kNanScale ? 0u : e2m1x8(z + 8 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            out[i] = s == kNanScale ? 0x7f7f7f7fu : e4m3x4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+    }
+}
+
+// SiLU(a) * b. exp(-a) may overflow to infinity: a / inf is the right 0.
+__device__ __forceinline__ float swiglu(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
+
+}  // namespace mx
+}  // namespace mxfp4

@@ -1,0 +1,110 @@
+// Activations as microscaled codes: z = x, or SiLU(gate) * up of rows
+// [gate | up], in fp32, then blocks of 32 (mx_common.cuh).
+//
+// A thread takes 16 values, half a block, at one place of the row and walks
+// down the rows, several rows' loads in flight; the block's maximum is one
+// shuffle between neighbours. Bound by HBM.
+//
+// The next kernel of the stream is not let in early: it may take these codes
+// as weights, and the library's products read weights before they wait for the
+// kernel ahead of them.
+#include "mx_common.cuh"
+#include "mx_launch.h"
+#include "step_common.cuh"
+
+namespace mxfp4 {
+namespace {
+
+struct QuantizeParams {
+    const __nv_bfloat16* x;
+    int64_t x_stride, t;
+    uint8_t *xq, *xs;
+    int halves;  // of a row: k / 16
+};
+
+struct alignas(16) Half {  // 16 bf16 values
+    Bf16x8 v[2];
+};
+
+__device__ __forceinline__ Half load_half(const __nv_bfloat16* p) {
+    Half h;
+    h.v[0] = *reinterpret_cast<const Bf16x8*>(p);
+    h.v[1] = *reinterpret_cast<const Bf16x8*>(p + 8);
+    return h;
+}
+
+template <bool SWIGLU, bool E2M1>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(QuantizeParams p) {
+    constexpr int U = SWIGLU ? 2 : 4;  // rows in flight
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    // Whole warps take part in the shuffles; a block's two threads have both work or none (halves is even).
+    const bool live = i < p.halves;
+    const int64_t k = static_cast<int64_t>(p.halves) * 16, at = live ? static_cast<int64_t>(i) * 16 : 0;
+    pdl_wait_previous();
+    for (int64_t row0 = blockIdx.y; row0 < p.t; row0 += static_cast<int64_t>(gridDim.y) * U) {
+        Half a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + static_cast<int64_t>(u) * gridDim.y;
+            if (row >= p.t) break;
+            const __nv_bfloat16* src = p.x + row * p.x_stride + at;
+            a[u] = load_half(src);
+            if constexpr (SWIGLU) b[u] = load_half(src + k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + static_cast<int64_t>(u) * gridDim.y;
+            if (row >= p.t) break;
+            float z[16];
+            unpack8(a[u].v[0], *reinterpret_cast<float(*)[8]>(z));
+            unpack8(a[u].v[1], *reinterpret_cast<float(*)[8]>(z + 8));
+            if constexpr (SWIGLU) {
+                float up[16];
+                unpack8(b[u].v[0], *reinterpret_cast<float(*)[8]>(up));
+                unpack8(b[u].v[1], *reinterpret_cast<float(*)[8]>(up + 8));
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = mx::swiglu(z[j], up[j]);
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = max(top, mx::abs_bits(z[j]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const uint32_t s = mx::scale_byte<E2M1>(top);
+            uint32_t w[E2M1 ? 2 : 4];
+            mx::encode<E2M1, 16>(z, s, w);
+            if (!live) continue;
+            const int64_t e = row * k + at;
+            if constexpr (E2M1)
+                *reinterpret_cast<uint2*>(p.xq + e / 2) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint4*>(p.xq + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            if ((i & 1) == 0) p.xs[e / 32] = static_cast<uint8_t>(s);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, int num_sms, cudaStream_t stream) {
+    QuantizeParams p{};
+    p.x = static_cast<const __nv_bfloat16*>(a.x);
+    p.x_stride = a.x_stride;
+    p.t = a.t;
+    p.xq = static_cast<uint8_t*>(a.xq);
+    p.xs = a.xs;
+    p.halves = static_cast<int>(a.k / 16);
+    // Blocks of at most 256 threads that cover the row evenly, in whole warps.
+    const int across = (p.halves + 255) / 256;
+    const int threads = ((p.halves + across - 1) / across + 31) / 32 * 32;
+    int64_t down = (static_cast<int64_t>(num_sms) * 8 + across - 1) / across;
+    if (down > a.t) down = a.t;
+    if (down > 65535) down = 65535;
+    PdlLaunch l(dim3(across, static_cast<unsigned>(down)), dim3(threads), 0, stream);
+    if (a.swiglu)
+        return a.e2m1 ? cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<true, true>, p)
+                      : cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<true, false>, p);
+    return a.e2m1 ? cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<false, true>, p)
+                  : cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<false, false>, p);
+}
+
+}  // namespace mxfp4

@@ -16,6 +16,7 @@
 // 4 tokens take 3.1 us, a launch.
 #include "step_launch.h"
 
+#include "mx_common.cuh"
 #include "step_common.cuh"
 
 namespace mxfp4 {
@@ -24,6 +25,7 @@ namespace {
 struct NormParams {
     const __nv_bfloat16 *x, *residual, *post_weight, *post_bias, *gate, *weight, *bias;
     __nv_bfloat16 *y, *r_out;
+    uint8_t *yq, *ys;     // y as codes and scales in its place
     int64_t gate_stride;  // elements between tokens; 0: one gate row for all
     int n, tokens;
     float scale, eps, weight_offset;
@@ -79,7 +81,31 @@ struct Row {
     }
 };
 
-template <int THREADS, int CH, bool VEC, bool LAYER>
+// How y leaves: bf16, or microscaled codes (VEC only).
+enum { kBf16, kE4M3, kE2M1 };
+
+// 8 values of y, at `at` of row t, as codes. Four neighbouring threads hold a
+// block of 32 (n % 32 == 0, so none straddles the row's end).
+template <bool E2M1>
+__device__ __forceinline__ void store_codes(const NormParams& p, int64_t row, int at, const float (&v)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, mx::abs_bits(v[j]));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t s = mx::scale_byte<E2M1>(top);
+    uint32_t w[E2M1 ? 1 : 2];
+    mx::encode<E2M1, 8>(v, s, w);
+    if (at >= p.n) return;
+    const int64_t e = row + at;
+    if constexpr (E2M1)
+        *reinterpret_cast<uint32_t*>(p.yq + e / 2) = w[0];
+    else
+        *reinterpret_cast<uint2*>(p.yq + e) = make_uint2(w[0], w[1]);
+    if ((threadIdx.x & 3) == 0) p.ys[e / 32] = static_cast<uint8_t>(s);
+}
+
+template <int THREADS, int CH, bool VEC, bool LAYER, int OUT>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(NormParams p) {
     using R = Row<THREADS, CH, VEC>;
     constexpr int WARPS = THREADS / 32;
@@ -172,7 +198,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(
 #pragma unroll
                 for (int j = 0; j < 8; ++j) r[c][j] += w[j];
             }
-            R::store_chunk(p.y + row, n, c, r[c]);
+            if constexpr (OUT == kBf16)
+                R::store_chunk(p.y + row, n, c, r[c]);
+            else
+                store_codes<OUT == kE2M1>(p, row, R::at(c, 0), r[c]);
         }
         if (!more) break;
         t = next;
@@ -182,14 +211,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(
 
 // Blocks for `per_sm` of them on each SM, or a row each if there are fewer.
 template <int THREADS, int CH>
-cudaError_t launch(const NormParams& p, int per_sm, int num_sms, bool vec, bool layer, cudaStream_t stream) {
+cudaError_t launch(const NormParams& p, int per_sm, int num_sms, bool vec, bool layer, int out, cudaStream_t stream) {
     const int blocks = p.tokens < per_sm * num_sms ? p.tokens : per_sm * num_sms;
     PdlLaunch l(dim3(blocks), dim3(THREADS), 0, stream);
+    auto go = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, p); };
+    if (p.yq && out == kE2M1)
+        return layer ? go(residual_norm_kernel<THREADS, CH, true, true, kE2M1>)
+                     : go(residual_norm_kernel<THREADS, CH, true, false, kE2M1>);
+    if (p.yq)
+        return layer ? go(residual_norm_kernel<THREADS, CH, true, true, kE4M3>)
+                     : go(residual_norm_kernel<THREADS, CH, true, false, kE4M3>);
     if (vec)
-        return layer ? cudaLaunchKernelEx(&l.cfg, residual_norm_kernel<THREADS, CH, true, true>, p)
-                     : cudaLaunchKernelEx(&l.cfg, residual_norm_kernel<THREADS, CH, true, false>, p);
-    return layer ? cudaLaunchKernelEx(&l.cfg, residual_norm_kernel<THREADS, CH, false, true>, p)
-                 : cudaLaunchKernelEx(&l.cfg, residual_norm_kernel<THREADS, CH, false, false>, p);
+        return layer ? go(residual_norm_kernel<THREADS, CH, true, true, kBf16>)
+                     : go(residual_norm_kernel<THREADS, CH, true, false, kBf16>);
+    return layer ? go(residual_norm_kernel<THREADS, CH, false, true, kBf16>)
+                 : go(residual_norm_kernel<THREADS, CH, false, false, kBf16>);
 }
 
 }  // namespace
@@ -203,7 +239,10 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, int num_sms, cudaStr
     p.gate = static_cast<const __nv_bfloat16*>(a.gate);
     p.weight = static_cast<const __nv_bfloat16*>(a.weight);
     p.bias = static_cast<const __nv_bfloat16*>(a.bias);
-    p.y = static_cast<__nv_bfloat16*>(a.y);
+    const int out = !a.ys ? kBf16 : a.e2m1 ? kE2M1 : kE4M3;
+    p.y = a.ys ? nullptr : static_cast<__nv_bfloat16*>(a.y);
+    p.yq = a.ys ? static_cast<uint8_t*>(a.y) : nullptr;
+    p.ys = a.ys;
     p.r_out = static_cast<__nv_bfloat16*>(a.r_out);
     p.gate_stride = a.gate_stride;
     p.n = static_cast<int>(a.n);
@@ -221,12 +260,12 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, int num_sms, cudaStr
     // 60; 8,192 of 4,096: 4 46, 2 56, 3 57; 4,096 of 7,168: 2 46, 1 57. Beyond
     // 16,384 columns a row's values spill: 2,048 rows of 18,432 take 193 us, 23 %
     // of the copy rate.
-    if (chunks <= 128) return launch<128, 1>(p, 8, num_sms, vec, a.layer, stream);
-    if (chunks <= 256) return launch<256, 1>(p, 4, num_sms, vec, a.layer, stream);
-    if (chunks <= 512) return launch<256, 2>(p, 4, num_sms, vec, a.layer, stream);
-    if (chunks <= 1024) return launch<512, 2>(p, 2, num_sms, vec, a.layer, stream);
-    if (chunks <= 2048) return launch<1024, 2>(p, 1, num_sms, vec, a.layer, stream);
-    return launch<1024, 4>(p, 1, num_sms, vec, a.layer, stream);
+    if (chunks <= 128) return launch<128, 1>(p, 8, num_sms, vec, a.layer, out, stream);
+    if (chunks <= 256) return launch<256, 1>(p, 4, num_sms, vec, a.layer, out, stream);
+    if (chunks <= 512) return launch<256, 2>(p, 4, num_sms, vec, a.layer, out, stream);
+    if (chunks <= 1024) return launch<512, 2>(p, 2, num_sms, vec, a.layer, out, stream);
+    if (chunks <= 2048) return launch<1024, 2>(p, 1, num_sms, vec, a.layer, out, stream);
+    return launch<1024, 4>(p, 1, num_sms, vec, a.layer, out, stream);
 }
 
 }  // namespace mxfp4

@@ -14,9 +14,11 @@ struct BatchView;
 struct ResidualNormArgs {
     const void *x, *residual, *post_weight, *post_bias, *gate, *weight, *bias;
     void *y, *r_out;
+    uint8_t* ys;  // null: y is bf16; otherwise y takes microscaled codes and this their scales
     int64_t tokens, n, gate_stride;
     float scale, eps, weight_offset;
     bool layer;
+    bool e2m1;    // type of the codes
 };
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, int num_sms, cudaStream_t stream);
 

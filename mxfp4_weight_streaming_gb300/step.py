@@ -194,11 +194,8 @@ class KVBatch:
         self.ref = ctypes.addressof(self.struct)
 
 
-def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=None, bias=None, scale=1.0, eps=1e-6,
-                  weight_offset=0.0, kind="rms", out=None, residual_out=None, stream=None):
-    """(y, r) of bf16 [tokens, n] x and residual: r = residual + scale * gate * u
-    with u = x or norm(x) * post_weight + post_bias, and y = norm(r) * weight + bias.
-    gate: [n] or [tokens, n]; kind "rms" or "layer"; weights count as weight + weight_offset."""
+def _norm_arguments(x, residual, weight, post_weight, post_bias, gate, bias, residual_out, kind):
+    """What residual_norm and residual_norm_mx check alike: (tokens, n, gate's stride)."""
     shape = x.shape
     if len(shape) != 2 or x.dtype is not _BF16 or residual.dtype is not _BF16 or residual.shape != shape or \
             not x.is_cuda or not x.is_contiguous() or not residual.is_contiguous():
@@ -213,11 +210,23 @@ def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=No
               "gate: bf16 [n] or [tokens, n] expected")
         if gate.dim() == 2:
             gate_stride = gate.stride(0) if t > 1 else n
-    for o in (out, residual_out):
-        if o is not None and (o.dtype is not _BF16 or o.shape != shape or not o.is_contiguous()):
-            raise ValueError("outputs: contiguous bf16 [tokens, n] expected")
+    if residual_out is not None and (residual_out.dtype is not _BF16 or residual_out.shape != shape or
+                                     not residual_out.is_contiguous()):
+        raise ValueError("outputs: contiguous bf16 [tokens, n] expected")
     if kind != "rms" and kind != "layer":
         raise ValueError("kind: 'rms' or 'layer' expected")
+    return t, n, gate_stride
+
+
+def residual_norm(x, residual, weight, post_weight=None, post_bias=None, gate=None, bias=None, scale=1.0, eps=1e-6,
+                  weight_offset=0.0, kind="rms", out=None, residual_out=None, stream=None):
+    """(y, r) of bf16 [tokens, n] x and residual: r = residual + scale * gate * u
+    with u = x or norm(x) * post_weight + post_bias, and y = norm(r) * weight + bias.
+    gate: [n] or [tokens, n]; kind "rms" or "layer"; weights count as weight + weight_offset."""
+    t, n, gate_stride = _norm_arguments(x, residual, weight, post_weight, post_bias, gate, bias, residual_out, kind)
+    shape = x.shape
+    if out is not None and (out.dtype is not _BF16 or out.shape != shape or not out.is_contiguous()):
+        raise ValueError("outputs: contiguous bf16 [tokens, n] expected")
     device = x.get_device()
     _on_device(device, residual, weight, post_weight, post_bias, gate, bias, out, residual_out)
     y = _made(stream, shape, _BF16, x.device) if out is None else out
