@@ -18,8 +18,8 @@
 //          accumulator, 32-column chunks by turns with warp w ^ 4
 //   8      copies codes (TMA) into a ring of stages
 //   9      issues the scales' copies into TMEM and the products
-//   10-12  scales: 128 tokens, and weight rows 0-127 and 128-255 of the tile.
-//          A lane holds rows l, l + 32, l + 64, l + 96 and writes the word of
+//   10-15  scales: 128 tokens, and weight rows 0-127 and 128-255 of the tile,
+//          two warps each. A lane holds rows l, l + 32, l + 64, l + 96 and writes the word of
 //          128 values of each as one 16-byte line, the layout that the copy
 //          into TMEM wants; the words of the next stages are loaded ahead
 // Two accumulators alternate, so the next tile's products run under the
@@ -28,6 +28,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <initializer_list>
+#include <mutex>
 
 #include "device_common.cuh"
 #include "mx_common.cuh"
@@ -39,15 +42,21 @@ namespace mxfp4 {
 namespace mxp {
 namespace {
 
-constexpr int kEpilogueWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 3;
+constexpr int kEpilogueWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 6;
 constexpr int kThreads = 32 * (kScaleWarp + kScaleWarps);
 constexpr int kRows = 128;                 // tokens of a tile
 constexpr int kStageRow = 128;             // bytes of a row in a stage
-constexpr int kStageA = kRows * kStageRow;
-constexpr int kMaxStages = 8;
-constexpr int kTmemCols = 512;
-constexpr int kAccCols = 432;              // two accumulators; one of 256 columns shares some with the other
+constexpr int kMaxStages = 16;
+constexpr int kGroupWords = 4;             // scale words (128 values each) of a row that are handled at a time
+constexpr int kMaxGroupSlots = 6;
+constexpr int kMaxColumnSlots = 4;         // of TMEM columns with scales
+constexpr int kAhead = 2;                  // groups that a warp loads ahead
+constexpr int kTmemCols = 512;             // all of them, so the allocation begins at column 0
 constexpr int kImage = 512;                // scales of 128 rows and 128 values
+
+// Columns for two accumulators (of 256 each they share some); the rest holds
+// scales, those of two stages at a time.
+__host__ __device__ constexpr int acc_cols(bool e2m1) { return e2m1 ? 416 : 432; }
 
 struct Params {
     const uint8_t *xs, *ws;
@@ -55,34 +64,55 @@ struct Params {
     unsigned* status;
     int64_t t, n, k;
     int m_tiles, tiles, width, stages;     // stages: of the whole k
-    int ring;                              // stages in shared memory
+    int ring, slots;                       // stages and groups of scales in shared memory
+    int split;                             // CTAs (or pairs) of a cluster that share a tile, each a part of k
     int rows_a, rows_b;                    // rows of a copied box
     bool out_e2m1;
-    bool wide;                             // 16-byte stores of y
+    int align;                             // bytes that every row of y begins at a multiple of (32, 16 or 2)
 };
 
+constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxGroupSlots + 4 + kMaxColumnSlots + 1;
 struct Bars {
     uint32_t base;
     __device__ uint32_t full(int s) const { return base + 8 * s; }
-    __device__ uint32_t scales(int s) const { return base + 8 * (kMaxStages + s); }
-    __device__ uint32_t empty(int s) const { return base + 8 * (2 * kMaxStages + s); }
-    __device__ uint32_t acc_full(int b) const { return base + 8 * (3 * kMaxStages + b); }
-    __device__ uint32_t acc_empty(int b) const { return base + 8 * (3 * kMaxStages + 2 + b); }
-    __device__ uint32_t drain() const { return base + 8 * (3 * kMaxStages + 4); }
+    __device__ uint32_t empty(int s) const { return base + 8 * (kMaxStages + s); }
+    __device__ uint32_t scales_full(int g) const { return base + 8 * (2 * kMaxStages + g); }
+    __device__ uint32_t scales_empty(int g) const { return base + 8 * (2 * kMaxStages + kMaxGroupSlots + g); }
+    __device__ uint32_t acc_full(int b) const { return base + 8 * (2 * kMaxStages + 2 * kMaxGroupSlots + b); }
+    __device__ uint32_t acc_empty(int b) const { return base + 8 * (2 * kMaxStages + 2 * kMaxGroupSlots + 2 + b); }
+    __device__ uint32_t columns_free(int s) const { return base + 8 * (2 * kMaxStages + 2 * kMaxGroupSlots + 4 + s); }
+    __device__ uint32_t drain() const { return base + 8 * (kNumBars - 1); }
 };
-constexpr int kNumBars = 3 * kMaxStages + 5;
 
 // Shared memory from a 1024-byte boundary: the ring (A then B of each stage),
-// the stages' scale images, barriers, abort flag, TMEM base.
+// the scale images of `slots` groups ([128 rows][word] each), barriers,
+// abort flag, TMEM base.
 struct Plan {
-    int stage, images, words;  // bytes of a stage; scale images of a stage; words of a row in a stage
-    __host__ __device__ Plan(int width, bool e2m1) {
-        stage = kStageA + width * kStageRow;
-        words = e2m1 ? 2 : 1;
-        images = (1 + (width + 127) / 128) * words;
+    int a, stage, sets, group;  // bytes of a stage's tokens, and of it all; sets of 128 rows with scales; bytes of a group's images
+    // A product reads 128 rows of tokens. Where there are fewer in all, the rows behind them are whatever lies there (of
+    // this stage's weights and what follows): each row of the result depends on its own token only. So a stage takes no
+    // more room than it has tokens, and the ring is deeper.
+    __host__ __device__ Plan(int width, int cg, int rows_a) {
+        a = rows_a * kStageRow;
+        stage = a + width / cg * kStageRow;
+        sets = 1 + (width + 127) / 128;
+        group = sets * kGroupWords * kImage;
     }
-    __host__ __device__ int bars_at(int ring) const { return ring * (stage + images * kImage); }
-    __host__ __device__ int bytes(int ring) const { return bars_at(ring) + 8 * kNumBars + 16 + 1024; }
+    __host__ __device__ int groups_at(int ring) const { return ring * stage; }
+    __host__ __device__ int bars_at(int ring, int slots) const {
+        const int end = groups_at(ring) + slots * group, read = (ring - 1) * stage + kRows * kStageRow;
+        return end > read ? end : read;
+    }
+    __host__ __device__ int bytes(int ring, int slots) const { return bars_at(ring, slots) + 8 * kNumBars + 16 + 1024; }
+};
+
+// What a CTA (or pair) works on: tiles first, first + step, ..., of each the
+// groups [group0, group0 + groups) of k, stages [stage0, stage0 + stages).
+struct Unit {
+    int first, step;
+    int group0, groups, stage0, stages;
+    int part;               // of the cluster's parts of k
+    uint32_t rank, leader;  // place in the pair; the cluster's rank of its first CTA
 };
 
 struct Ring {
@@ -106,86 +136,145 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Wa
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
 }
 
+// Arrives on an mbarrier of the pair's first CTA, which issues the products.
+// Without release at cluster scope, which waits for every load that the SM has
+// under way (2,000 cycles): no memory is handed from one CTA to the other here.
+// Scales are read, and accumulators were, where the arriving warp wrote or read
+// them, by tensor-core instructions that start after this arrival.
+__device__ __forceinline__ void arrive_at_first(uint32_t bar, const Unit& u) {
+    if (u.rank == 0)
+        mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, u.leader)) : "memory");
+}
+
 // Tile -> its first token and its first output. Tokens run fastest, in groups
 // of 16 tiles, so that a wave of tiles reads few weight rows and its tokens stay in L2.
-template <bool SWIGLU>
+template <int CG, bool SWIGLU>
 __device__ __forceinline__ void place(const Params& p, int tile, int64_t& t0, int64_t& n0) {
     constexpr int kGroup = 16;
     const int n_tiles = p.tiles / p.m_tiles;
     const int group = tile / (kGroup * n_tiles), in = tile - group * kGroup * n_tiles;
     const int high = min(kGroup, p.m_tiles - group * kGroup);
     const int nt = in / high;
-    t0 = static_cast<int64_t>(group * kGroup + in - nt * high) * kRows;
+    t0 = static_cast<int64_t>(group * kGroup + in - nt * high) * (CG * kRows);
     n0 = static_cast<int64_t>(nt) * (SWIGLU ? p.width / 2 : p.width);
 }
 
 // ---------------------------------------------------------------- copies
-template <bool E2M1, bool SWIGLU>
-__device__ void copy_codes(const Params& p, const Plan& plan, const CUtensorMap* amap, const CUtensorMap* bmap,
-                           uint32_t base, const Bars& bars, const WaitCtx& wc) {
-    const uint32_t bytes = p.rows_a * kStageRow + p.width * (E2M1 ? kStageRow : kStageRow / 2);
-    Ring r;
-    int issued = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < p.tiles && ok; tile += gridDim.x) {
-        int64_t t0, n0;
-        place<SWIGLU>(p, tile, t0, n0);
-        for (int k = 0; k < p.stages; ++k) {
-            if (!mbar_wait(bars.empty(r.slot), r.phase ^ 1u, wc)) {
-                ok = false;
-                break;
-            }
-            const uint32_t a = base + r.slot * plan.stage, b = a + kStageA, full = bars.full(r.slot);
-            ++issued;
-            if (withhold_stage(static_cast<uint32_t>(issued - 1))) {  // test-only builds
-                r.next(p.ring);
-                continue;
-            }
-            mbar_arrive_expect_tx(full, bytes);
-            tc::load_box_2d(a, amap, k * kStageRow, static_cast<int>(t0), full);
-            auto weights = [&](uint32_t dst, int64_t row) {
-                if constexpr (E2M1)
-                    tc::load_box_2d(dst, bmap, k * kStageRow, static_cast<int>(row), full);
-                else
-                    tc::load_box_3d(dst, bmap, 0, static_cast<int>(row), k, full);
-            };
-            weights(b, n0);
-            if constexpr (SWIGLU) weights(b + p.rows_b * kStageRow, p.n + n0);
-            r.next(p.ring);
-        }
+template <int CG, bool E2M1, bool SWIGLU>
+struct Copier {
+    const Params& p;
+    const Plan& plan;
+    const Unit& u;
+    const CUtensorMap *amap, *bmap;
+    uint32_t base;
+    const Bars& bars;
+    int first;           // stages of the first tile that fill the ring
+    int64_t t0, n0;
+
+    __device__ __forceinline__ Copier(const Params& p_, const Plan& plan_, const Unit& u_, const CUtensorMap* a,
+                                      const CUtensorMap* b, uint32_t base_, const Bars& bars_)
+        : p(p_), plan(plan_), u(u_), amap(a), bmap(b), base(base_), bars(bars_) {
+        first = u.first < p.tiles ? min(p.ring, u.stages) : 0;
+        place<CG, SWIGLU>(p, u.first, t0, n0);
     }
-    if (!ok) {
-        // Copies in flight land before the CTA may exit (bounded, whatever the abort flag says).
+    // A stage's bytes, of both CTAs of a pair, complete on the first one's barrier.
+    __device__ __forceinline__ uint32_t full(int slot) const {
+        return CG == 1 ? bars.full(slot) : map_to_rank(bars.full(slot), u.leader);
+    }
+    __device__ __forceinline__ void codes(uint32_t dst, const CUtensorMap* map, int k, int64_t y, uint32_t bar) const {
+        if constexpr (CG == 1)
+            tc::load_box_2d(dst, map, k * kStageRow, static_cast<int>(y), bar);
+        else
+            tc::load_box_2d_pair(dst, map, k * kStageRow, static_cast<int>(y), bar);
+    }
+    __device__ __forceinline__ void weight_box(uint32_t dst, int k, int64_t y, uint32_t bar) const {
+        if constexpr (E2M1)
+            codes(dst, bmap, k, y, bar);
+        else if constexpr (CG == 1)
+            tc::load_box_3d(dst, bmap, 0, static_cast<int>(y), k, bar);
+        else
+            tc::load_box_3d_pair(dst, bmap, 0, static_cast<int>(y), k, bar);
+    }
+    // Weight rows of this CTA: a pair's CTAs take a half of the tile each, which is the gate rows and the up rows in the
+    // gated form.
+    __device__ __forceinline__ void weights(int slot, int k) const {
+        const uint32_t b = base + slot * plan.stage + plan.a, bar = full(slot);
+        if (u.rank == 0)
+            mbar_arrive_expect_tx(bars.full(slot),
+                                  CG * p.rows_a * kStageRow + p.width * (E2M1 ? kStageRow : kStageRow / 2));
+        weight_box(b, k, CG == 1 ? n0 : SWIGLU ? n0 + u.rank * p.n : n0 + u.rank * p.rows_b, bar);
+        if constexpr (SWIGLU && CG == 1) weight_box(b + p.rows_b * kStageRow, k, p.n + n0, bar);
+    }
+    __device__ __forceinline__ void tokens(int slot, int k) const {
+        codes(base + slot * plan.stage, amap, k, t0 + u.rank * kRows, full(slot));
+    }
+    // The weights of the ring's first round. They do not wait for the previous kernel of the stream.
+    __device__ __forceinline__ void begin() const {
+        for (int j = 0; j < first; ++j)
+            if (!withhold_stage(static_cast<uint32_t>(j))) weights(j, u.stage0 + j);
+    }
+    __device__ __forceinline__ void run(const WaitCtx& wc) {
+        pdl_wait_previous();  // it may still write the tokens
+        for (int j = 0; j < first; ++j)
+            if (!withhold_stage(static_cast<uint32_t>(j))) tokens(j, u.stage0 + j);
+        Ring r;
+        int issued = 0;
+        bool ok = true;
+        for (int tile = u.first; tile < p.tiles && ok; tile += u.step) {
+            place<CG, SWIGLU>(p, tile, t0, n0);
+            for (int k = u.stage0; k < u.stage0 + u.stages; ++k) {
+                if (issued >= first) {
+                    if (!mbar_wait(bars.empty(r.slot), r.phase ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    weights(r.slot, k);
+                    tokens(r.slot, k);
+                }
+                ++issued;
+                r.next(p.ring);
+            }
+        }
+        if (!ok) drain(issued);
+    }
+    // Copies in flight land before the CTA may exit (bounded, whatever the abort flag says).
+    __device__ __forceinline__ void drain(int issued) const {
         int never = 0;
         const WaitCtx own{p.status, &never};
-        for (int j = issued > p.ring ? issued - p.ring : 0; j < issued; ++j)
-            mbar_wait(bars.full(j % p.ring), static_cast<uint32_t>((j / p.ring) & 1), own);
+        if (u.rank == 0) {
+            for (int j = issued > p.ring ? issued - p.ring : 0; j < issued; ++j)
+                mbar_wait(bars.full(j % p.ring), static_cast<uint32_t>((j / p.ring) & 1), own);
+        } else {
+            // Theirs complete on the other CTA's barrier, which cannot be waited for from here: a box lands within
+            // microseconds.
+            const uint64_t begin = global_timer_ns();
+            while (global_timer_ns() - begin < 2000000ull) __nanosleep(1000);
+        }
     }
-}
+};
 
 // ---------------------------------------------------------------- scales
-// Warp `image` of the scale warps: image 0 tokens, 1 and 2 weight rows.
-template <bool E2M1, bool SWIGLU>
-__device__ void copy_scales(const Params& p, const Plan& plan, int image, int lane, uint32_t base, const Bars& bars,
+// Warp `set` of the scale warps: set 0 tokens, 1 and 2 weight rows.
+template <int CG, bool SWIGLU>
+__device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, int set, int turn, int lane, uint32_t base, const Bars& bars,
                             const WaitCtx& wc) {
-    constexpr int W = E2M1 ? 2 : 1;   // words of a row in a stage
-    constexpr int S = 4 / W;          // stages of a group of 4 words
     const int64_t pitch = p.k / 32;
     const int words = static_cast<int>(p.k / 128);
-    const uint8_t* array = image == 0 ? p.xs : p.ws;
+    const uint8_t* array = set == 0 ? p.xs : p.ws;
     const bool wide = pitch % 16 == 0 && (reinterpret_cast<uintptr_t>(array) & 15) == 0;
-    const int groups = (p.stages + S - 1) / S;
-
     const uint8_t* row[4];
     auto rows_of = [&](int tile) {
         int64_t t0, n0;
-        place<SWIGLU>(p, tile, t0, n0);
+        place<CG, SWIGLU>(p, tile, t0, n0);
+        t0 += u.rank * kRows;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int r = 32 * q + lane + 128 * (image - 1);
+            const int r = 32 * q + lane + 128 * (set - 1);
             int64_t at;
             bool valid;
-            if (image == 0) {
+            if (set == 0) {
                 at = t0 + 32 * q + lane;
                 valid = at < p.t;
             } else if (!SWIGLU) {
@@ -200,114 +289,186 @@ __device__ void copy_scales(const Params& p, const Plan& plan, int image, int la
             row[q] = valid ? array + at * pitch : nullptr;
         }
     };
-    uint4 v[4];
-    auto load = [&](int g) {
+    // The set's other warp takes every second group, and each has its next kAhead groups on their way in registers: a
+    // group of 512 values is multiplied in 0.3 us and more, its loads from HBM take over 1 us, and getting it into place
+    // some 1,000 cycles.
+    uint4 v[kAhead][4];
+    int tile = u.first, g = u.group0;  // the next group to load
+    bool turned = true;                // the rows are not this tile's yet
+    auto skip = [&] {
+        if (++g == u.group0 + u.groups) {
+            g = u.group0;
+            tile = u.step < p.tiles - tile ? tile + u.step : p.tiles;
+            turned = true;
+        }
+    };
+    auto load = [&](uint4 (&to)[4]) {
+        if (tile >= p.tiles) return;
+        if (turned) rows_of(tile);
+        turned = false;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            v[q] = make_uint4(0u, 0u, 0u, 0u);  // rows that do not exist: their results go nowhere
+            to[q] = make_uint4(0u, 0u, 0u, 0u);  // rows that do not exist: their results go nowhere
             if (!row[q]) continue;
             // Through L2: another kernel may have written them just now.
             if (wide) {
-                v[q] = __ldcg(reinterpret_cast<const uint4*>(row[q]) + g);
+                to[q] = __ldcg(reinterpret_cast<const uint4*>(row[q]) + g);
             } else {
-                const uint32_t* s = reinterpret_cast<const uint32_t*>(row[q]) + 4 * g;
-                if (4 * g < words) v[q].x = __ldcg(s);
-                if (4 * g + 1 < words) v[q].y = __ldcg(s + 1);
-                if (4 * g + 2 < words) v[q].z = __ldcg(s + 2);
-                if (4 * g + 3 < words) v[q].w = __ldcg(s + 3);
+                const uint32_t* s = reinterpret_cast<const uint32_t*>(row[q]) + kGroupWords * g;
+                const int left = words - kGroupWords * g;
+                to[q].x = __ldcg(s);
+                if (left > 1) to[q].y = __ldcg(s + 1);
+                if (left > 2) to[q].z = __ldcg(s + 2);
+                if (left > 3) to[q].w = __ldcg(s + 3);
             }
         }
+        skip();
+        if (tile < p.tiles) skip();
     };
+    // This CTA's groups in all, and this warp's first.
+    int64_t left = u.first < p.tiles ? static_cast<int64_t>((p.tiles - u.first + u.step - 1) / u.step) * u.groups : 0;
     Ring r;
-    if (static_cast<int>(blockIdx.x) < p.tiles) {
-        rows_of(blockIdx.x);
-        load(0);
+    if (turn) {
+        --left;
+        if (tile < p.tiles) skip();
+        r.next(p.slots);
     }
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-        for (int g = 0; g < groups; ++g) {
-            uint4 now[4] = {v[0], v[1], v[2], v[3]};
-            if (g + 1 < groups) {
-                load(g + 1);
-            } else if (static_cast<int>(gridDim.x) < p.tiles - tile) {
-                rows_of(tile + gridDim.x);
-                load(0);
-            }
-            const uint32_t* a = reinterpret_cast<const uint32_t*>(now);
+    if (set == 0) pdl_wait_previous();  // the tokens may come from the previous kernel, weights do not
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                if (g * S + s >= p.stages) break;
-                if (!wait_all(bars.empty(r.slot), r.phase ^ 1u, wc)) return;
-                const uint32_t at = base + p.ring * plan.stage + (r.slot * plan.images + image * W) * kImage + lane * 16;
+    for (int d = 0; d < kAhead; ++d) load(v[d]);
+    while (left > 0) {
 #pragma unroll
-                for (int w = 0; w < W; ++w)
-                    sts128(at + w * kImage, a[s * W + w], a[4 + s * W + w], a[8 + s * W + w], a[12 + s * W + w]);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.scales(r.slot));
-                r.next(p.ring);
-            }
+        for (int d = 0; d < kAhead; ++d) {
+            if (left <= 0) break;
+            left -= 2;
+            if (!wait_all(bars.scales_empty(r.slot), r.phase ^ 1u, wc)) return;
+            const uint4(&w)[4] = v[d];
+            const uint32_t at = base + plan.groups_at(p.ring) + r.slot * plan.group + set * kGroupWords * kImage + lane * 16;
+            sts128(at, w[0].x, w[1].x, w[2].x, w[3].x);
+            sts128(at + kImage, w[0].y, w[1].y, w[2].y, w[3].y);
+            sts128(at + 2 * kImage, w[0].z, w[1].z, w[2].z, w[3].z);
+            sts128(at + 3 * kImage, w[0].w, w[1].w, w[2].w, w[3].w);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) arrive_at_first(bars.scales_full(r.slot), u);
+            load(v[d]);
+            r.next(p.slots);
+            r.next(p.slots);
         }
     }
 }
 
 // -------------------------------------------------------------- products
-template <bool E2M1>
-__device__ bool issue_products(const Params& p, const Plan& plan, uint32_t base, uint32_t tbase, const Bars& bars,
+// The instructions of one CTA or of a pair.
+template <int CG>
+__device__ __forceinline__ void copy_scales_to_tmem(uint32_t taddr, uint64_t desc) {
+    if constexpr (CG == 1)
+        tc::copy_scales_to_tmem(taddr, desc);
+    else
+        tc::copy_scales_to_tmem_pair(taddr, desc);
+}
+template <int CG>
+__device__ __forceinline__ void commit_to(uint32_t bar, const Unit& u) {
+    if constexpr (CG == 1)
+        tc::commit_to(bar);
+    else
+        tc::commit_to_pair(bar, static_cast<uint16_t>(3u << u.leader));
+}
+template <int CG>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         bool acc) {
+    if constexpr (CG == 1)
+        tc::mma_mxf8f6f4(d, a, b, idesc, sfa, sfb, acc);
+    else
+        tc::mma_mxf8f6f4_pair(d, a, b, idesc, sfa, sfb, acc);
+}
+template <int CG>
+__device__ __forceinline__ void mma_e2m1(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         bool acc) {
+    if constexpr (CG == 1)
+        tc::mma_mxf4(d, a, b, idesc, sfa, sfb, acc);
+    else
+        tc::mma_mxf4_pair(d, a, b, idesc, sfa, sfb, acc);
+}
+
+template <int CG, bool E2M1>
+__device__ bool issue_products(const Params& p, const Plan& plan, const Unit& u, uint32_t base, const Bars& bars,
                                const WaitCtx& wc) {
-    // TMEM scale slots above the accumulators, 4 columns an image. A slot is
-    // written again only after the products that read it are done.
-    const int slots = (kTmemCols - kAccCols) / (4 * plan.images);
+    // Two stages are waited for and issued together: a round of waiting and issuing costs some 300 cycles whatever is
+    // issued, the products of a stage take 256 to 512.
+    constexpr int W = E2M1 ? 2 : 1;       // scale words of a row in a stage
+    constexpr int S = kGroupWords / W;    // stages of a group of scales
+    constexpr int kAccCols = acc_cols(E2M1);
+    // TMEM scale slots above the accumulators, 4 columns an image: of each word the tokens', then the weight rows' sets. A
+    // slot is written again only after the products that read it are done.
+    const int word_cols = 4 * plan.sets, slot_cols = 2 * W * word_cols;
+    const int slots = min((kTmemCols - kAccCols) / slot_cols, kMaxColumnSlots);
     const bool shared_cols = 2 * p.width > kAccCols;
-    const int sfb_col = 4 * plan.words;
     const uint32_t idesc = tc::mma_idesc(E2M1 ? tc::kFmtMxf4E2M1 : tc::kFmtE4M3, E2M1 ? tc::kFmtMxf4E2M1 : tc::kFmtE2M1,
-                                         kRows, static_cast<uint32_t>(p.width), 0);
+                                         CG * kRows, static_cast<uint32_t>(p.width), 0);
+    // All lanes walk through the stages and one issues, so that the operands stay in uniform registers (one lane alone took
+    // twice the time a product).
     const bool one = elect_one();
-    Ring r, behind;  // behind: the stage `slots` before
-    int it = 0, tslot = 0, i = 0;
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++i) {
+    Ring r, gr, tr;
+    int rounds = 0, i = 0;
+    for (int tile = u.first; tile < p.tiles; tile += u.step, ++i) {
         const int back = shared_cols ? 1 : 2;  // whose epilogue frees this accumulator
         if (i >= back && !wait_all(bars.acc_empty(i & 1), static_cast<uint32_t>((i - back) >> 1) & 1u, wc)) return false;
-        const uint32_t d = tbase + ((i & 1) ? kAccCols - p.width : 0);
-        for (int k = 0; k < p.stages; ++k, ++it) {
-            if (slots < p.ring && it >= slots) {
-                if (!wait_all(bars.empty(behind.slot), behind.phase, wc)) return false;
-                behind.next(p.ring);
-            }
-            if (!wait_all(bars.scales(r.slot), r.phase, wc)) return false;
-            if (!wait_all(bars.full(r.slot), r.phase, wc)) return false;
-            tc::fence_after_sync();
-            const uint32_t a = base + r.slot * plan.stage;
-            const uint32_t image = base + p.ring * plan.stage + r.slot * plan.images * kImage;
-            const uint32_t sf = tbase + kAccCols + tslot * 4 * plan.images;
-            const uint64_t ad = tc::operand_desc(a), bd = tc::operand_desc(a + kStageA), sd = tc::scale_image_desc(image);
+        tc::fence_after_sync();
+        const uint32_t d = (i & 1) ? kAccCols - p.width : 0;
+        for (int k = 0; k < u.stages; k += 2, ++rounds) {
+            const int n = min(2, u.stages - k), in = k % S;
+            Ring r1 = r;
+            if (n == 2) r1.next(p.ring);
+            const uint32_t fb = bars.full(r.slot), fb1 = bars.full(r1.slot);
+            const uint32_t b2 = in == 0 ? bars.scales_full(gr.slot) : fb, p2 = in == 0 ? gr.phase : r.phase;
+            const uint32_t b3 = rounds >= slots ? bars.columns_free(tr.slot) : fb, p3 = rounds >= slots ? tr.phase ^ 1u : r.phase;
+            while (!__all_sync(0xffffffffu, mbar_test4(fb, r.phase, fb1, r1.phase, b2, p2, b3, p3)))
+                if (!wait_all(b3, p3, wc) || !wait_all(b2, p2, wc) || !wait_all(fb, r.phase, wc) ||
+                    !wait_all(fb1, r1.phase, wc))
+                    return false;
+            const uint32_t images = base + plan.groups_at(p.ring) + gr.slot * plan.group + in * W * kImage;
+            const uint32_t sf = kAccCols + tr.slot * slot_cols;
+            const uint64_t sd = tc::scale_image_desc(images);
+            const bool last = k + n == u.stages, ends = in + 2 >= S || last;
             if (one) {
-                // Images in memory: of the tokens by word, then of each 128 weight rows by word. In TMEM the weight
-                // rows' images of one word lie next to each other.
+                // The images of both stages, in memory [set][word] (there are four words to a group, whatever k).
 #pragma unroll
-                for (int w = 0; w < (E2M1 ? 2 : 1); ++w) {
-                    tc::copy_scales_to_tmem(sf + 4 * w, sd + w * (kImage >> 4));
-                    for (int b = 0; b * 128 < p.width; ++b)
-                        tc::copy_scales_to_tmem(sf + sfb_col + (w * ((p.width + 127) / 128) + b) * 4,
-                                                sd + ((1 + b) * plan.words + w) * (kImage >> 4));
+                for (int w = 0; w < 2 * W; ++w) {
+                    copy_scales_to_tmem<CG>(sf + w * word_cols, sd + w * (kImage >> 4));
+                    copy_scales_to_tmem<CG>(sf + w * word_cols + 4, sd + (kGroupWords + w) * (kImage >> 4));
+                    if (plan.sets > 2) copy_scales_to_tmem<CG>(sf + w * word_cols + 8, sd + (2 * kGroupWords + w) * (kImage >> 4));
                 }
+                // They are free once they are in TMEM.
+                if (ends) commit_to<CG>(bars.scales_empty(gr.slot), u);
+            }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const bool acc = k != 0 || c != 0;
-                    if constexpr (E2M1) {
-                        const uint32_t sfb = sf + sfb_col + (c >> 1) * ((p.width + 127) / 128) * 4;
-                        tc::mma_mxf4(d, ad + 2 * c, bd + 2 * c, idesc | ((c & 1) * 2u) << 4 | ((c & 1) * 2u) << 29,
-                                     sf + 4 * (c >> 1), sfb, acc);
-                    } else {
-                        tc::mma_mxf8f6f4(d, ad + 2 * c, bd + 2 * c,
-                                         idesc | static_cast<uint32_t>(c) << 4 | static_cast<uint32_t>(c) << 29, sf,
-                                         sf + sfb_col, acc);
+            for (int j = 0; j < 2; ++j) {
+                if (j == 1 && n == 1) break;
+                const uint32_t a = base + (j ? r1.slot : r.slot) * plan.stage;
+                const uint64_t ad = tc::operand_desc(a), bd = tc::operand_desc(a + plan.a);
+                if (one) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const bool acc = k != 0 || j != 0 || c != 0;
+                        const uint32_t sfa = sf + (j * W + (E2M1 ? c >> 1 : 0)) * word_cols;
+                        if constexpr (E2M1)
+                            mma_e2m1<CG>(d, ad + 2 * c, bd + 2 * c, idesc | ((c & 1) * 2u) << 4 | ((c & 1) * 2u) << 29, sfa,
+                                         sfa + 4, acc);
+                        else
+                            mma_e4m3<CG>(d, ad + 2 * c, bd + 2 * c,
+                                         idesc | static_cast<uint32_t>(c) << 4 | static_cast<uint32_t>(c) << 29, sfa, sfa + 4,
+                                         acc);
                     }
+                    commit_to<CG>(bars.empty(j ? r1.slot : r.slot), u);
+                    if (j == n - 1) commit_to<CG>(bars.columns_free(tr.slot), u);
+                    if (last && j == n - 1) commit_to<CG>(bars.acc_full(i & 1), u);
                 }
-                tc::commit_to(bars.empty(r.slot));
-                if (k == p.stages - 1) tc::commit_to(bars.acc_full(i & 1));
             }
             __syncwarp();
-            if (++tslot == slots) tslot = 0;
+            if (ends) gr.next(p.slots);
+            tr.next(slots);
+            r = r1;
             r.next(p.ring);
         }
     }
@@ -320,15 +481,30 @@ __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
     tc::tmem_load<32>(taddr, r);
 }
 
-// 32 outputs of one token, `count` of them wanted.
-__device__ __forceinline__ void store_row(__nv_bfloat16* y, const float (&v)[32], int count, bool wide) {
-    if (wide && count >= 32) {
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 32 outputs of one token, `count` of them wanted. align: bytes that every row begins at a multiple of.
+__device__ __forceinline__ void store_row(__nv_bfloat16* y, const float (&v)[32], int count, int align) {
+    if (align >= 16 && count >= 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+            w[q] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (align >= 32) {
+            store32(y, *reinterpret_cast<const uint32_t(*)[8]>(w));
+            store32(y + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 8));
+            return;
+        }
         uint4* o = reinterpret_cast<uint4*>(y);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const Bf16x8 b = pack8(*reinterpret_cast<const float(*)[8]>(v + 8 * q));
-            o[q] = *reinterpret_cast<const uint4*>(&b);
-        }
+        for (int q = 0; q < 4; ++q) o[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         return;
     }
 #pragma unroll
@@ -344,14 +520,38 @@ __device__ __forceinline__ void store_block(uint8_t* q, uint8_t* s, const float 
     const uint32_t b = mx::scale_byte<OUT_E2M1>(top);
     uint32_t w[OUT_E2M1 ? 4 : 8];
     mx::encode<OUT_E2M1, 32>(h, b, w);
+    if constexpr (OUT_E2M1)
+        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if (reinterpret_cast<uintptr_t>(q) % 32 == 0)
+        store32(q, w);
+    else
 #pragma unroll
-    for (int i = 0; i < (OUT_E2M1 ? 1 : 2); ++i)
-        reinterpret_cast<uint4*>(q)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 2; ++i)
+            reinterpret_cast<uint4*>(q)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     *s = static_cast<uint8_t>(b);
 }
 
+// 32 sums of one token at output `col`, or 32 of both of its halves (gate a, up b).
 template <bool SWIGLU>
-__device__ void epilogue(const Params& p, int warp, int lane, uint32_t tbase, const Bars& bars, const WaitCtx& wc) {
+__device__ __forceinline__ void finish(const Params& p, int64_t row, int64_t col, float (&a)[32], const float (&b)[32]) {
+    if (row >= p.t || col >= p.n) return;
+    if constexpr (SWIGLU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a[j] = mx::swiglu(a[j], b[j]);
+        const int64_t e = row * p.n + col;
+        if (p.out_e2m1)
+            store_block<true>(p.y + e / 2, p.ys + e / 32, a);
+        else
+            store_block<false>(p.y + e, p.ys + e / 32, a);
+    } else {
+        store_row(reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col, a,
+                  static_cast<int>(p.n - col < 32 ? p.n - col : 32), p.align);
+    }
+}
+
+template <int CG, bool SWIGLU>
+__device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, const Bars& bars, const WaitCtx& wc,
+                         int kAccCols) {
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const bool shared_cols = 2 * p.width > kAccCols;
@@ -359,127 +559,369 @@ __device__ void epilogue(const Params& p, int warp, int lane, uint32_t tbase, co
     // Chunks that hold columns of the other accumulator come first.
     const int early = shared_cols ? (2 * p.width - kAccCols + 31) / 32 : chunks;
     int i = 0;
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++i) {
+    for (int tile = u.first; tile < p.tiles; tile += u.step, ++i) {
         int64_t t0, n0;
-        place<SWIGLU>(p, tile, t0, n0);
+        place<CG, SWIGLU>(p, tile, t0, n0);
+        t0 += u.rank * kRows;
         if (!wait_all(bars.acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u, wc)) return;
         tc::fence_after_sync();
-        const uint32_t acc = tbase + lanes + ((i & 1) ? kAccCols - p.width : 0);
+        const uint32_t acc = lanes + ((i & 1) ? kAccCols - p.width : 0);
         const int64_t row = t0 + quarter * 32 + lane;
         for (int c = 0; c <= chunks; ++c) {
-            if (c == early || (c == chunks && early > chunks)) {
+            if (c == early) {
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars.acc_empty((i & 1) ^ (shared_cols ? 1 : 0)));
+                const uint32_t freed = bars.acc_empty((i & 1) ^ (shared_cols ? 1 : 0));
+                if (lane == 0) arrive_at_first(freed, u);
             }
             if (c == chunks) break;
             if ((c & 1) != half) continue;
             const int at = (i & 1) || !shared_cols ? c : chunks - 1 - c;
-            const int64_t col = n0 + 32 * at;
-            if constexpr (SWIGLU) {
-                float a[32], b[32];
-                load32(acc + 32 * at, a);
-                load32(acc + p.width / 2 + 32 * at, b);
-                tc::tmem_wait_ld();
-                if (row < p.t && col < p.n) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) a[j] = mx::swiglu(a[j], b[j]);
-                    const int64_t e = row * p.n + col;
-                    if (p.out_e2m1)
-                        store_block<true>(p.y + e / 2, p.ys + e / 32, a);
-                    else
-                        store_block<false>(p.y + e, p.ys + e / 32, a);
-                }
-            } else {
-                float v[32];
-                load32(acc + 32 * at, v);
-                tc::tmem_wait_ld();
-                if (row < p.t && col < p.n)
-                    store_row(reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col, v,
-                              static_cast<int>(p.n - col < 32 ? p.n - col : 32), p.wide);
-            }
+            float a[32], b[32];
+            load32(acc + 32 * at, a);
+            if constexpr (SWIGLU) load32(acc + p.width / 2 + 32 * at, b);
+            tc::tmem_wait_ld();
+            finish<SWIGLU>(p, row, n0 + 32 * at, a, b);
         }
     }
 }
 
+// The end of a tile whose k is split over a cluster: chunk c of the columns
+// belongs to part c % split, whose CTA takes the others' sums of it into its
+// ring (free by then) and adds them in the parts' order, so results do not
+// depend on who comes first.
+//   box (chunk c / split, sender): [8 or 2 x 8 pieces of 4 fp32][128 tokens], so
+//   that a warp's store is 512 bytes in a row (stores of 16 bytes 128 apart
+//   took 3 us longer a tile)
+template <bool SWIGLU>
+struct Exchange {
+    static constexpr int kHalves = SWIGLU ? 2 : 1;
+    static constexpr int kBox = kRows * 128 * kHalves;
+    const Params& p;
+    const Unit& u;
+    uint32_t base;
+    int cg, chunks;
+    __device__ Exchange(const Params& p_, const Unit& u_, uint32_t base_, int cg_)
+        : p(p_), u(u_), base(base_), cg(cg_), chunks((SWIGLU ? p_.width / 2 : p_.width) / 32) {}
+    __device__ uint32_t box(int c, int sender, int h, int token) const {
+        const int place = (c / p.split) * (p.split - 1) + sender - (sender > c % p.split ? 1 : 0);
+        return base + (place * kHalves + h) * kRows * 128 + token * 16;
+    }
+    __device__ void send(int warp, int lane, int64_t t0) const {
+        const int quarter = warp & 3, token = quarter * 32 + lane;
+        if (t0 + quarter * 32 >= p.t) return;  // the whole warp has no token
+        for (int c = warp >> 2; c < chunks; c += 2) {
+            const int owner = c % p.split;
+            if (owner == u.part) continue;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                float v[32];
+                load32((static_cast<uint32_t>(quarter * 32) << 16) + h * (p.width / 2) + 32 * c, v);
+                tc::tmem_wait_ld();
+                const uint32_t to = map_to_rank(box(c, u.part, h, token), static_cast<uint32_t>(owner * cg) + u.rank);
+                if (t0 + token < p.t) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        st_cluster_f32x4(to + q * kRows * 16, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+            }
+        }
+    }
+    __device__ void add(float (&v)[32], int c, int h, int token) const {
+        for (int s = 0; s < p.split; ++s) {
+            if (s == u.part) continue;
+            const uint32_t from = box(c, s, h, token);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint4 w = lds128(from + q * kRows * 16);
+                v[4 * q] += __uint_as_float(w.x);
+                v[4 * q + 1] += __uint_as_float(w.y);
+                v[4 * q + 2] += __uint_as_float(w.z);
+                v[4 * q + 3] += __uint_as_float(w.w);
+            }
+        }
+    }
+    __device__ void receive(int warp, int lane, int64_t t0, int64_t n0) const {
+        const int quarter = warp & 3, token = quarter * 32 + lane;
+        if (t0 + quarter * 32 >= p.t) return;
+        for (int c = u.part + (warp >> 2) * p.split; c < chunks; c += 2 * p.split) {
+            const uint32_t acc = (static_cast<uint32_t>(quarter * 32) << 16) + 32 * c;
+            float a[32], b[32];
+            load32(acc, a);
+            if constexpr (SWIGLU) load32(acc + p.width / 2, b);
+            tc::tmem_wait_ld();
+            add(a, c, 0, token);
+            if constexpr (SWIGLU) add(b, c, 1, token);
+            finish<SWIGLU>(p, t0 + token, n0 + 32 * c, a, b);
+        }
+    }
+};
+
 // ---------------------------------------------------------------- kernel
-template <bool E2M1, bool SWIGLU>
+template <int CG, bool E2M1, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx_product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p) {
+    mx_product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                      const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const Plan plan(p.width, E2M1);
+    const Plan plan(p.width, CG, p.rows_a);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Bars bars{base + plan.bars_at(p.ring)};
+    Unit u;
+    {
+        constexpr int kGroupStages = kGroupWords / (E2M1 ? 2 : 1);
+        const int cluster = CG * p.split;
+        const uint32_t in = blockIdx.x % cluster;
+        const int groups = (p.stages + kGroupStages - 1) / kGroupStages;
+        u.first = static_cast<int>(blockIdx.x) / cluster;
+        u.step = static_cast<int>(gridDim.x) / cluster;
+        u.part = static_cast<int>(in) / CG;
+        u.rank = in % CG;
+        u.leader = in - u.rank;
+        u.group0 = groups * u.part / p.split;
+        u.groups = groups * (u.part + 1) / p.split - u.group0;
+        u.stage0 = u.group0 * kGroupStages;
+        u.stages = min(u.groups * kGroupStages, p.stages - u.stage0);
+    }
+    const Bars bars{base + plan.bars_at(p.ring, p.slots)};
     const uint32_t flag = bars.base + 8 * kNumBars, tslot = flag + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (flag - raw));
     const WaitCtx wc{p.status, abort_flag};
     pdl_launch_dependents();
-    if (warp == kMmaWarp) {
-        tc::tmem_alloc(tslot, kTmemCols);
-        tc::tmem_relinquish();
-    }
     if (warp == kCopyWarp && lane == 0) {
-        for (int s = 0; s < p.ring; ++s) {
-            mbar_init(bars.full(s), 1);
-            mbar_init(bars.scales(s), static_cast<uint32_t>(plan.images / plan.words));
-            mbar_init(bars.empty(s), 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(bars.acc_full(b), 1);
-            mbar_init(bars.acc_empty(b), kEpilogueWarps);
-        }
-        mbar_init(bars.drain(), 1);
-        *abort_flag = 0;
-        fence_barrier_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&bmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&amap) : "memory");
     }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tbase = lds_u32_volatile(tslot);
-    // Codes and scales may come from the previous kernel of the stream, and it may still read y.
-    pdl_wait_previous();
+    if (warp == kMmaWarp) {
+        if constexpr (CG == 1) {
+            tc::tmem_alloc(tslot, kTmemCols);
+            tc::tmem_relinquish();
+        } else {
+            tc::tmem_alloc_pair(tslot, kTmemCols);
+            tc::tmem_relinquish_pair();
+        }
+    }
+    // Barriers are the copying warp's, which goes on to the first copies while the others wait for them and for TMEM.
+    const bool alone = CG == 1 && p.split == 1;
+    Copier<CG, E2M1, SWIGLU> copier(p, plan, u, &amap, &bmap, base, bars);
+    if (warp == kCopyWarp) {
+        if (lane == 0) {
+            for (int s = 0; s < p.ring; ++s) {
+                mbar_init(bars.full(s), 1);
+                mbar_init(bars.empty(s), 1);
+            }
+            for (int g = 0; g < p.slots; ++g) {
+                mbar_init(bars.scales_full(g), static_cast<uint32_t>(CG * plan.sets));
+                mbar_init(bars.scales_empty(g), 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(bars.acc_full(b), 1);
+                mbar_init(bars.acc_empty(b), CG * kEpilogueWarps);
+            }
+            for (int s = 0; s < kMaxColumnSlots; ++s) mbar_init(bars.columns_free(s), 1);
+            mbar_init(bars.drain(), 1);
+            *abort_flag = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
+        if (alone)
+            asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (lane == 0 && u.rank == 0) copier.begin();  // on barriers of its own
+        __syncwarp();
+        if (!alone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        tc::fence_before_sync();
+        if (alone)
+            asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        else
+            cluster_sync_all();
+        tc::fence_after_sync();
+    }
+    bool summed = true;
     if (warp < kEpilogueWarps) {
-        epilogue<SWIGLU>(p, warp, lane, tbase, bars, wc);
+        pdl_wait_previous();  // the previous kernel may still use what y is written over
+        if (p.split == 1)
+            epilogue<CG, SWIGLU>(p, u, warp, lane, bars, wc, acc_cols(E2M1));
+        else
+            summed = wait_all(bars.acc_full(0), 0, wc);  // a cluster has one tile
     } else if (warp == kCopyWarp) {
-        if (lane == 0) copy_codes<E2M1, SWIGLU>(p, plan, &amap, &bmap, base, bars, wc);
+        if (lane == 0) {
+            if (u.rank != 0) copier.begin();
+            copier.run(wc);
+        }
     } else if (warp == kMmaWarp) {
-        if (!issue_products<E2M1>(p, plan, base, tbase, bars, wc)) {
+        if (u.rank == 0 && !issue_products<CG, E2M1>(p, plan, u, base, bars, wc)) {
             // Products issued so far may still read shared memory and write TMEM: waited for, bounded.
             if (lane == 0) {
-                tc::commit_to(bars.drain());
+                commit_to<CG>(bars.drain(), u);
                 int never = 0;
                 const WaitCtx own{p.status, &never};
                 mbar_wait(bars.drain(), 0, own);
             }
         }
-    } else if ((warp - kScaleWarp) * plan.words < plan.images) {
-        copy_scales<E2M1, SWIGLU>(p, plan, warp - kScaleWarp, lane, base, bars, wc);
+    } else if ((warp - kScaleWarp) % 3 < plan.sets) {
+        copy_scales<CG, SWIGLU>(p, plan, u, (warp - kScaleWarp) % 3, (warp - kScaleWarp) / 3, lane, base, bars, wc);
     }
     __syncwarp();
+    if (p.split > 1) {
+        const Exchange<SWIGLU> ex(p, u, base, CG);
+        int64_t t0, n0;
+        place<CG, SWIGLU>(p, u.first, t0, n0);
+        t0 += u.rank * kRows;
+        tc::fence_after_sync();
+        cluster_sync_all();  // every part is summed: the rings are free
+        if (warp < kEpilogueWarps && summed) ex.send(warp, lane, t0);
+        __syncwarp();
+        cluster_sync_all();
+        if (warp < kEpilogueWarps && summed) ex.receive(warp, lane, t0, n0);
+        __syncwarp();
+    }
     tc::fence_before_sync();
-    __syncthreads();
+    // A CTA of a pair stays until the other's copies, arrivals and products on it are done.
+    if constexpr (CG == 1)
+        __syncthreads();
+    else
+        cluster_sync_all();
     if (warp == kMmaWarp) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tbase, kTmemCols);
+        if constexpr (CG == 1)
+            tc::tmem_dealloc(0, kTmemCols);
+        else
+            tc::tmem_dealloc_pair(0, kTmemCols);
     }
 }
 
-template <bool E2M1, bool SWIGLU>
-cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, int grid,
+// ------------------------------------------------------------------ host
+template <int CG, bool E2M1, bool SWIGLU>
+cudaError_t configure(int smem) {
+    return cudaFuncSetAttribute(mx_product_kernel<CG, E2M1, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+template <int CG, bool E2M1, bool SWIGLU>
+cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, int grid, bool overlap,
                    cudaStream_t stream) {
-    static int configured[64] = {0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || configured[dev] < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(mx_product_kernel<E2M1, SWIGLU>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev] = smem;
-    }
     PdlLaunch l(dim3(grid), dim3(kThreads), smem, stream);
-    return cudaLaunchKernelEx(&l.cfg, mx_product_kernel<E2M1, SWIGLU>, amap, bmap, p);
+    if (!overlap) l.cfg.numAttrs = 0;
+    if (CG * p.split > 1) {
+        cudaLaunchAttribute& cluster = l.attr[l.cfg.numAttrs++];
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim.x = CG * p.split;
+        cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    }
+    return cudaLaunchKernelEx(&l.cfg, mx_product_kernel<CG, E2M1, SWIGLU>, amap, bmap, p);
+}
+
+template <int CG>
+cudaError_t launch_any(bool e2m1, bool swiglu, const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p,
+                       int smem, int grid, bool overlap, cudaStream_t stream) {
+    if (e2m1)
+        return swiglu ? launch<CG, true, true>(amap, bmap, p, smem, grid, overlap, stream)
+                      : launch<CG, true, false>(amap, bmap, p, smem, grid, overlap, stream);
+    return swiglu ? launch<CG, false, true>(amap, bmap, p, smem, grid, overlap, stream)
+                  : launch<CG, false, false>(amap, bmap, p, smem, grid, overlap, stream);
+}
+
+// What the choice of a tile needs to know of a device.
+struct Device {
+    bool ready;
+    int sms, max_smem;
+    int clusters[9];  // of so many CTAs, one to an SM, that are resident at once
+};
+
+cudaError_t device_of(const Device** out, int num_sms, int max_smem) {
+    static Device devices[64];
+    static std::mutex mutex;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    Device& d = devices[dev];
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!d.ready) {
+        cudaError_t e = cudaSuccess;
+        for (auto set : {configure<1, false, false>, configure<1, false, true>, configure<1, true, false>,
+                         configure<1, true, true>, configure<2, false, false>, configure<2, false, true>,
+                         configure<2, true, false>, configure<2, true, true>})
+            if ((e = set(max_smem))) return e;
+        d.sms = num_sms;
+        d.max_smem = max_smem;
+        d.clusters[1] = num_sms;
+        for (int c = 2; c <= 8; ++c) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = c;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(c * num_sms);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = max_smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&d.clusters[c], mx_product_kernel<1, false, false>, &cfg))) return e;
+        }
+        d.ready = true;
+    }
+    *out = &d;
+    return cudaSuccess;
+}
+
+// A tile's shape and the CTAs that share its k.
+struct Choice {
+    int cg, width, split, ring, slots, smem;
+    float us;
+};
+
+// Stages in the ring, and slots for the scales of as many and two groups more; false if not even two fit.
+bool fit(Choice& c, int rows_a, bool e2m1, int max_smem) {
+    const Plan plan(c.width, c.cg, rows_a);
+    auto slots_for = [&](int ring) {
+        const int s = (ring * (e2m1 ? 2 : 1) + kGroupWords - 1) / kGroupWords + 2;
+        return s < kMaxGroupSlots ? s : kMaxGroupSlots;
+    };
+    c.ring = 1;
+    while (c.ring < kMaxStages && plan.bytes(c.ring + 1, slots_for(c.ring + 1)) <= max_smem) ++c.ring;
+    c.slots = slots_for(c.ring);
+    c.smem = plan.bytes(c.ring, c.slots);
+    return c.ring > 1;
+}
+
+// The tile with the least time by a model of what was measured on GB300 (in
+// CUDA graphs, us):
+//   a stage of a CTA   0.14 + 0.0008 width (width 64 0.22, 128 0.24, 192 0.27-0.33, 256 0.30-0.42: its copies and
+//                      products share the bandwidth of shared memory, 128 bytes a cycle)
+//   a stage of a pair  0.13 + 0.0007 width (128 0.19-0.24, 192 0.20-0.30, 256 0.24-0.38: each CTA reads half the
+//                      weights), for twice the tokens
+//   a launch           4.5 (a pair 5.5): first copies, last products, the stores
+//   a shared tile      1.7 and 20 KB a us for the sums that a CTA hands on
+// A part of k less per CTA only pays while every tile is on the GPU at once.
+Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, const Device& d) {
+    const int stages = static_cast<int>((k + (e2m1 ? 255 : 127)) / (e2m1 ? 256 : 128));
+    const int groups = static_cast<int>((k / 128 + kGroupWords - 1) / kGroupWords);
+    const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows;
+    Choice best{};
+    best.us = 1e30f;
+    for (int cg = 1; cg <= (t > kRows ? 2 : 1); ++cg) {
+        for (int width = swiglu ? 64 : 32; width <= 256; width += swiglu ? 64 : 32) {
+            const int outputs = swiglu ? width / 2 : width;
+            const float stage = cg == 1 ? 0.14f + 0.0008f * width : 0.13f + 0.0007f * width;
+            const int64_t tiles = ((t + kRows * cg - 1) / (kRows * cg)) * ((n + outputs - 1) / outputs);
+            for (int split = 1; split * cg <= 8 && split <= groups; ++split) {
+                if (split > 1 && tiles > d.clusters[cg * split]) break;
+                Choice c{cg, width, split, 0, 0, 0, 0.f};
+                const int64_t waves = (tiles + d.clusters[cg] - 1) / d.clusters[cg];
+                const int longest = (groups + split - 1) / split * (kGroupWords / (e2m1 ? 2 : 1));
+                c.us = (split > 1 ? 1 : waves) * stage * (longest < stages ? longest : stages) + (cg == 1 ? 4.5f : 5.5f);
+                if (split > 1) c.us += 1.7f + rows_a * width * 4.f * (split - 1) / split / 20e3f;
+                if (c.us >= best.us || !fit(c, rows_a, e2m1, d.max_smem)) continue;
+                // The sums of the others have to fit the ring (chunks of 32 columns, of both halves where swiglu).
+                const int inbox = (outputs / 32 + split - 1) / split * (split - 1) * kRows * 128 * (swiglu ? 2 : 1);
+                if (inbox > c.ring * Plan(width, cg, rows_a).stage) continue;
+                best = c;
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -487,8 +929,23 @@ cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Param
 
 cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem, cudaStream_t stream) {
     using namespace mxp;
-    const int width = 256;
-    const int outputs = a.swiglu ? width / 2 : width;
+    const Device* device = nullptr;
+    if (cudaError_t e = device_of(&device, num_sms, max_smem)) return e;
+    // The choice takes some 10 us of host time: the last sizes' are kept.
+    struct Kept {
+        int64_t t, n, k;
+        const Device* device;
+        int kind;
+        Choice choice;
+    };
+    thread_local Kept kept[16];
+    const int kind = (a.e2m1 ? 2 : 0) + (a.swiglu ? 1 : 0);
+    Kept& slot = kept[(a.t * 31 + a.n * 7 + a.k / 128 + kind) & 15];
+    if (slot.device != device || slot.t != a.t || slot.n != a.n || slot.k != a.k || slot.kind != kind)
+        slot = Kept{a.t, a.n, a.k, device, kind, choose(a.t, a.n, a.k, a.e2m1, a.swiglu, *device)};
+    const Choice& c = slot.choice;
+    if (!c.cg) return cudaErrorInvalidValue;
+    const int outputs = a.swiglu ? c.width / 2 : c.width, rows = kRows * c.cg;
     Params p{};
     p.xs = a.xs;
     p.ws = a.ws;
@@ -498,19 +955,20 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     p.t = a.t;
     p.n = a.n;
     p.k = a.k;
-    p.width = width;
+    p.width = c.width;
+    p.split = c.split;
+    p.ring = c.ring;
+    p.slots = c.slots;
     p.out_e2m1 = a.out_e2m1;
-    p.wide = a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(2 * a.n);
+    p.align = rows_at % 32 == 0 ? 32 : rows_at % 16 == 0 ? 16 : 2;
     p.stages = static_cast<int>((a.k + (a.e2m1 ? 255 : 127)) / (a.e2m1 ? 256 : 128));
-    const int64_t m_tiles = (a.t + kRows - 1) / kRows, n_tiles = (a.n + outputs - 1) / outputs;
-    if (m_tiles * n_tiles >= (int64_t(1) << 31) - num_sms) return cudaErrorInvalidValue;
+    const int64_t m_tiles = (a.t + rows - 1) / rows, n_tiles = (a.n + outputs - 1) / outputs;
+    if (m_tiles * n_tiles >= (int64_t(1) << 27)) return cudaErrorInvalidValue;
     p.m_tiles = static_cast<int>(m_tiles);
     p.tiles = static_cast<int>(m_tiles * n_tiles);
     p.rows_a = a.t < kRows ? static_cast<int>((a.t + 7) / 8 * 8) : kRows;
-    p.rows_b = outputs;
-    const Plan plan(width, a.e2m1);
-    p.ring = 1;
-    while (p.ring < kMaxStages && plan.bytes(p.ring + 1) <= max_smem) ++p.ring;
+    p.rows_b = a.swiglu || c.cg == 2 ? c.width / 2 : c.width;
     const int64_t w_rows = a.swiglu ? 2 * a.n : a.n;
     CUtensorMap amap, bmap;
     cudaError_t e = encode_code_map(&amap, a.xq, a.t, a.e2m1 ? a.k / 2 : a.k, p.rows_a);
@@ -518,13 +976,11 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
         e = a.e2m1 ? encode_code_map(&bmap, a.wq, w_rows, a.k / 2, p.rows_b)
                    : encode_spread_map(&bmap, a.wq, w_rows, a.k, p.rows_b);
     if (e != cudaSuccess) return e;
-    const int grid = p.tiles < num_sms ? p.tiles : num_sms;
-    const int smem = plan.bytes(p.ring);
-    if (a.e2m1)
-        return a.swiglu ? launch<true, true>(amap, bmap, p, smem, grid, stream)
-                        : launch<true, false>(amap, bmap, p, smem, grid, stream);
-    return a.swiglu ? launch<false, true>(amap, bmap, p, smem, grid, stream)
-                    : launch<false, false>(amap, bmap, p, smem, grid, stream);
+    const int cluster = c.cg * c.split, most = device->clusters[c.cg];
+    const int grid = cluster * (c.split > 1 || p.tiles < most ? p.tiles : most);
+    const bool overlap = worth_overlap(stream, c.us);
+    return c.cg == 1 ? launch_any<1>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, overlap, stream)
+                     : launch_any<2>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, overlap, stream);
 }
 
 }  // namespace mxfp4

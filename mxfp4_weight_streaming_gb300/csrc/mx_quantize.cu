@@ -100,6 +100,7 @@ cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, int num_sms, cudaStream_
     if (down > a.t) down = a.t;
     if (down > 65535) down = 65535;
     PdlLaunch l(dim3(across, static_cast<unsigned>(down)), dim3(threads), 0, stream);
+    if (!worth_overlap(stream, 2.f + 1e-6f * a.t * a.k * (a.swiglu ? 5 : 3) / 6.f)) l.cfg.numAttrs = 0;
     if (a.swiglu)
         return a.e2m1 ? cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<true, true>, p)
                       : cudaLaunchKernelEx(&l.cfg, mx_quantize_kernel<true, false>, p);
