@@ -800,10 +800,9 @@ cudaError_t configure(int smem) {
 }
 
 template <int CG, bool E2M1, bool SWIGLU>
-cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, int grid, bool overlap,
+cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, int grid,
                    cudaStream_t stream) {
     PdlLaunch l(dim3(grid), dim3(kThreads), smem, stream);
-    if (!overlap) l.cfg.numAttrs = 0;
     if (CG * p.split > 1) {
         cudaLaunchAttribute& cluster = l.attr[l.cfg.numAttrs++];
         cluster.id = cudaLaunchAttributeClusterDimension;
@@ -815,12 +814,12 @@ cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Param
 
 template <int CG>
 cudaError_t launch_any(bool e2m1, bool swiglu, const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p,
-                       int smem, int grid, bool overlap, cudaStream_t stream) {
+                       int smem, int grid, cudaStream_t stream) {
     if (e2m1)
-        return swiglu ? launch<CG, true, true>(amap, bmap, p, smem, grid, overlap, stream)
-                      : launch<CG, true, false>(amap, bmap, p, smem, grid, overlap, stream);
-    return swiglu ? launch<CG, false, true>(amap, bmap, p, smem, grid, overlap, stream)
-                  : launch<CG, false, false>(amap, bmap, p, smem, grid, overlap, stream);
+        return swiglu ? launch<CG, true, true>(amap, bmap, p, smem, grid, stream)
+                      : launch<CG, true, false>(amap, bmap, p, smem, grid, stream);
+    return swiglu ? launch<CG, false, true>(amap, bmap, p, smem, grid, stream)
+                  : launch<CG, false, false>(amap, bmap, p, smem, grid, stream);
 }
 
 // What the choice of a tile needs to know of a device.
@@ -978,9 +977,8 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     if (e != cudaSuccess) return e;
     const int cluster = c.cg * c.split, most = device->clusters[c.cg];
     const int grid = cluster * (c.split > 1 || p.tiles < most ? p.tiles : most);
-    const bool overlap = worth_overlap(stream, c.us);
-    return c.cg == 1 ? launch_any<1>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, overlap, stream)
-                     : launch_any<2>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, overlap, stream);
+    return c.cg == 1 ? launch_any<1>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream)
+                     : launch_any<2>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream);
 }
 
 }  // namespace mxfp4

@@ -214,8 +214,6 @@ template <int THREADS, int CH>
 cudaError_t launch(const NormParams& p, int per_sm, int num_sms, bool vec, bool layer, int out, cudaStream_t stream) {
     const int blocks = p.tokens < per_sm * num_sms ? p.tokens : per_sm * num_sms;
     PdlLaunch l(dim3(blocks), dim3(THREADS), 0, stream);
-    // (The bf16 form always begins early.)
-    if (p.yq && !worth_overlap(stream, 2.f + 1e-6f * p.tokens * static_cast<float>(p.n) * 8 / 6.f)) l.cfg.numAttrs = 0;
     auto go = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, p); };
     if (p.yq && out == kE2M1)
         return layer ? go(residual_norm_kernel<THREADS, CH, true, true, kE2M1>)

@@ -135,18 +135,4 @@ struct PdlLaunch {
     }
 };
 
-// Whether a launch that takes about `us` on the GPU should begin early. On the
-// GPU that always gains a microsecond or two; on the host such a launch next to
-// allocations of PyTorch's takes 5 us more (9.4 against 5.1), and short calls
-// are bound by the host. In a graph the host does not count.
-inline bool worth_overlap(cudaStream_t stream, float us) {
-    if (us > 12.f) return true;
-    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
-        cudaGetLastError();  // the legacy stream next to a capture: nothing of ours
-        return false;
-    }
-    return status == cudaStreamCaptureStatusActive;
-}
-
 }  // namespace mxfp4
