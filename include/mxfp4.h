@@ -528,6 +528,7 @@ int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* ba
  * are rounded to nearest, ties to even. A block that holds a NaN or an
  * infinity gets scale 255, NaN, and every output it takes part in is NaN.
  * (mxfp4_quantize's rule for weights is another: theirs may saturate.)
+ * Outputs may not overlap inputs or each other (but r_out may be residual or x).
  */
 typedef enum {
     MXFP4_MX_E4M3 = 0, /* 8 bits: 4 significant ones, 8.25 bits a value in all */
@@ -548,7 +549,7 @@ int mxfp4_quantize_mx(const void* x, int64_t x_stride, int64_t t, int64_t k, int
  *   n       a multiple of 32, at most 32768; every pointer but ys 16-byte
  *           aligned, gate_stride % 8 == 0
  *   yq, ys  device codes and scales of y (outputs)
- * Every other argument is as there; r_out may be residual.
+ * Every other argument is as there; r_out may be residual or x.
  */
 int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, int64_t n, const void* post_weight,
                            const void* post_bias, const void* gate, int64_t gate_stride, float scale,
@@ -557,12 +558,12 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
 
 /*
  * y[i][j] = bf16( sum_k x[i][k] * w[j][k] ) for any number of tokens.
- *   xq, xs  device MX codes and scales of x [t, k], 16-byte aligned; format:
- *           theirs
+ *   xq, xs  device MX codes (16-byte aligned) and scales (4-byte aligned) of x
+ *           [t, k]; format: theirs
  *   k       a multiple of 128
  *   wq, ws  device uint8 [n, k/2], [n, k/32], MXFP4 weights as for
- *           mxfp4_linear (scale bytes up to 254), 16-byte aligned (wq with
- *           E4M3 activations: 32)
+ *           mxfp4_linear, wq 16-byte aligned (with E4M3 activations 32), ws 4;
+ *           a scale byte of 255 is NaN
  *   y       device bf16 [t, n], 2-byte aligned (output; 16-byte aligned with
  *           n % 8 == 0 takes the wide stores)
  * Products of codes are exact, sums fp32 in the tensor cores' order. Codes and

@@ -1,5 +1,7 @@
 // C ABI of a prompt chunk's way through MXFP4 weights: argument checks, then
 // the launches of mx_quantize.cu, mx_product.cu and norm.cu.
+#include <initializer_list>
+
 #include "mx_launch.h"
 #include "step_common.cuh"
 #include "step_launch.h"
@@ -13,6 +15,30 @@ int launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUD
 bool known(int format) { return format == MXFP4_MX_E4M3 || format == MXFP4_MX_E2M1; }
 
 constexpr int64_t kMost = int64_t(1) << 31;  // coordinates of a copy are ints
+constexpr int64_t kMostStride = int64_t(1) << 31;
+
+// Memory of an operand. Outputs may not lie in the inputs: rows are read and
+// written by different blocks in any order.
+struct Range {
+    const void* at;
+    int64_t bytes;
+    bool meets(const Range& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+        return at && o.at && a < b + o.bytes && b < a + bytes;
+    }
+};
+
+bool any_meet(std::initializer_list<Range> outputs, std::initializer_list<Range> inputs) {
+    for (const Range& o : outputs) {
+        for (const Range& i : inputs)
+            if (o.meets(i)) return true;
+        for (const Range& p : outputs)
+            if (&p != &o && o.meets(p)) return true;
+    }
+    return false;
+}
+
+int64_t code_bytes(int64_t values, int format) { return format == MXFP4_MX_E2M1 ? values / 2 : values; }
 
 int product(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq, const uint8_t* ws,
             int64_t n, bool swiglu, int out_format, void* y, uint8_t* ys, void* stream) {
@@ -21,9 +47,13 @@ int product(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k,
         return MXFP4_ERR_INVALID_ARG;
     if (k % 128 || k >= kMost || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
         return MXFP4_ERR_SHAPE;
-    for (const void* p : {xq, static_cast<const void*>(xs), static_cast<const void*>(ws)})
-        if (!aligned(p, 16)) return MXFP4_ERR_ALIGN;
-    if (!aligned(wq, format == MXFP4_MX_E4M3 ? 32 : 16) || !aligned(y, swiglu ? 16 : 2)) return MXFP4_ERR_ALIGN;
+    if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(wq, format == MXFP4_MX_E4M3 ? 32 : 16) ||
+        !aligned(y, swiglu ? 16 : 2))
+        return MXFP4_ERR_ALIGN;
+    const int64_t rows = swiglu ? 2 * n : n;
+    const Range in[] = {{xq, code_bytes(t * k, format)}, {xs, t * k / 32}, {wq, rows * k / 2}, {ws, rows * k / 32}};
+    if (any_meet({{y, swiglu ? code_bytes(t * n, out_format) : 2 * t * n}, {ys, t * n / 32}}, {in[0], in[1], in[2], in[3]}))
+        return MXFP4_ERR_INVALID_ARG;
     mxfp4::DeviceCaps caps;
     if (int rc = mxfp4::device_caps(&caps)) return rc;
     mxfp4::MxProductArgs a{};
@@ -51,13 +81,16 @@ int mxfp4_quantize_mx(const void* x, int64_t x_stride, int64_t t, int64_t k, int
                       uint8_t* xs, void* stream) {
     if (!x || !xq || !xs || t <= 0 || k <= 0 || !known(format) || (x_stride && x_stride < (swiglu ? 2 : 1) * k))
         return MXFP4_ERR_INVALID_ARG;
-    if (k % 32 || k >= kMost || t >= kMost) return MXFP4_ERR_SHAPE;
+    if (k % 32 || k >= kMost || t >= kMost || x_stride >= kMostStride) return MXFP4_ERR_SHAPE;
     if (!aligned(x, 16) || x_stride % 8 || !aligned(xq, 16)) return MXFP4_ERR_ALIGN;
+    const int64_t width = (swiglu ? 2 : 1) * k, stride = x_stride ? x_stride : width;
+    if (any_meet({{xq, code_bytes(t * k, format)}, {xs, t * k / 32}}, {{x, 2 * ((t - 1) * stride + width)}}))
+        return MXFP4_ERR_INVALID_ARG;
     mxfp4::DeviceCaps caps;
     if (int rc = mxfp4::device_caps(&caps)) return rc;
     mxfp4::MxQuantizeArgs a{};
     a.x = x;
-    a.x_stride = x_stride ? x_stride : (swiglu ? 2 : 1) * k;
+    a.x_stride = stride;
     a.t = t;
     a.k = k;
     a.xq = xq;
@@ -72,13 +105,18 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
                            const void* weight, const void* bias, float weight_offset, float eps, int layer, int format,
                            void* yq, uint8_t* ys, void* r_out, void* stream) {
     if (!x || !residual || !weight || !yq || !ys || !r_out || tokens <= 0 || n <= 0 || (post_bias && !post_weight) ||
-        gate_stride < 0 || (gate_stride && gate_stride < n) || !(eps >= 0.f) || !known(format) || yq == r_out)
+        gate_stride < 0 || (gate_stride && gate_stride < n) || !(eps >= 0.f) || !known(format))
         return MXFP4_ERR_INVALID_ARG;
-    if (n > 32768 || n % 32 || tokens >= kMost) return MXFP4_ERR_SHAPE;
+    if (n > 32768 || n % 32 || tokens >= kMost || gate_stride >= kMostStride) return MXFP4_ERR_SHAPE;
     for (const void* p : {x, residual, post_weight, post_bias, gate, weight, bias, static_cast<const void*>(yq),
                           static_cast<const void*>(r_out)})
         if (!aligned(p, 16)) return MXFP4_ERR_ALIGN;
     if (gate_stride % 8) return MXFP4_ERR_ALIGN;
+    const Range r{r_out, 2 * tokens * n}, codes{yq, code_bytes(tokens * n, format)}, scales{ys, tokens * n / 32};
+    const int64_t gate_bytes = gate ? 2 * ((tokens - 1) * gate_stride + n) : 0;
+    if (any_meet({codes, scales}, {r, {x, 2 * tokens * n}, {residual, 2 * tokens * n}, {gate, gate_bytes}, {weight, 2 * n},
+                                   {bias, 2 * n}, {post_weight, 2 * n}, {post_bias, 2 * n}}))
+        return MXFP4_ERR_INVALID_ARG;
     mxfp4::DeviceCaps caps;
     if (int rc = mxfp4::device_caps(&caps)) return rc;
     mxfp4::ResidualNormArgs a{};

@@ -52,6 +52,7 @@ constexpr int kMaxGroupSlots = 6;
 constexpr int kMaxColumnSlots = 4;         // of TMEM columns with scales
 constexpr int kAhead = 2;                  // groups that a warp loads ahead
 constexpr int kTmemCols = 512;             // all of them, so the allocation begins at column 0
+constexpr int kTurn = 32 * 68;              // a warp's 32 x 32 outputs on their way to rows that are not aligned
 constexpr int kImage = 512;                // scales of 128 rows and 128 values
 
 // Columns for two accumulators (of 256 each they share some); the rest holds
@@ -86,7 +87,7 @@ struct Bars {
 
 // Shared memory from a 1024-byte boundary: the ring (A then B of each stage),
 // the scale images of `slots` groups ([128 rows][word] each), barriers,
-// abort flag, TMEM base.
+// abort flag, TMEM base, room to turn unaligned outputs round.
 struct Plan {
     int a, stage, sets, group;  // bytes of a stage's tokens, and of it all; sets of 128 rows with scales; bytes of a group's images
     // A product reads 128 rows of tokens. Where there are fewer in all, the rows behind them are whatever lies there (of
@@ -103,7 +104,10 @@ struct Plan {
         const int end = groups_at(ring) + slots * group, read = (ring - 1) * stage + kRows * kStageRow;
         return end > read ? end : read;
     }
-    __host__ __device__ int bytes(int ring, int slots) const { return bars_at(ring, slots) + 8 * kNumBars + 16 + 1024; }
+    __host__ __device__ int turn_at(int ring, int slots) const { return bars_at(ring, slots) + 8 * kNumBars + 16; }
+    __host__ __device__ int bytes(int ring, int slots, bool turn) const {
+        return turn_at(ring, slots) + (turn ? kEpilogueWarps * kTurn : 0) + 1024;
+    }
 };
 
 // What a CTA (or pair) works on: tiles first, first + step, ..., of each the
@@ -488,28 +492,48 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// 32 outputs of one token, `count` of them wanted. align: bytes that every row begins at a multiple of.
-__device__ __forceinline__ void store_row(__nv_bfloat16* y, const float (&v)[32], int count, int align) {
-    if (align >= 16 && count >= 32) {
-        uint32_t w[16];
+// The warp's 32 tokens x 32 outputs, lane i's of token `row`, `count` of them
+// wanted. Rows that begin at any even address go through shared memory: 64 bytes
+// of a token are written by 32 threads then (a thread's own 32 stores of 2 bytes
+// each touch a sector of their own).
+__device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64_t row, int64_t col, const float (&v)[32]) {
+    const int count = static_cast<int>(p.n - col < 32 ? p.n - col : 32), lane = threadIdx.x & 31;
+    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col;
+    uint32_t w[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-            w[q] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        if (align >= 32) {
+    for (int q = 0; q < 16; ++q) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+        w[q] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (p.align >= 16) {
+        if (row >= p.t) return;
+        if (count < 32) {  // a multiple of 8
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                if (8 * q < count)
+                    reinterpret_cast<uint4*>(y)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        } else if (p.align >= 32) {
             store32(y, *reinterpret_cast<const uint32_t(*)[8]>(w));
             store32(y + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 8));
-            return;
-        }
-        uint4* o = reinterpret_cast<uint4*>(y);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            for (int q = 0; q < 4; ++q)
+                reinterpret_cast<uint4*>(y)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < count) y[j] = __float2bfloat16_rn(v[j]);
+    for (int q = 0; q < 16; ++q)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(turn + lane * 68 + 4 * q), "r"(w[q]) : "memory");
+    __syncwarp();
+    const int rows = static_cast<int>(p.t - (row - lane) < 32 ? p.t - (row - lane) : 32);
+    uint16_t* to = reinterpret_cast<uint16_t*>(p.y) + (row - lane) * p.n + col + lane;
+    for (int i = 0; i < rows; ++i, to += p.n) {
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(turn + i * 68 + 2 * lane) : "memory");
+        if (lane < count) *to = h;
+    }
+    __syncwarp();
 }
 
 template <bool OUT_E2M1>
@@ -533,9 +557,11 @@ __device__ __forceinline__ void store_block(uint8_t* q, uint8_t* s, const float 
 
 // 32 sums of one token at output `col`, or 32 of both of its halves (gate a, up b).
 template <bool SWIGLU>
-__device__ __forceinline__ void finish(const Params& p, int64_t row, int64_t col, float (&a)[32], const float (&b)[32]) {
-    if (row >= p.t || col >= p.n) return;
+__device__ __forceinline__ void finish(const Params& p, uint32_t turn, int64_t row, int64_t col, float (&a)[32],
+                                       const float (&b)[32]) {
+    if (col >= p.n || row - (threadIdx.x & 31) >= p.t) return;  // none of the warp's tokens
     if constexpr (SWIGLU) {
+        if (row >= p.t) return;
 #pragma unroll
         for (int j = 0; j < 32; ++j) a[j] = mx::swiglu(a[j], b[j]);
         const int64_t e = row * p.n + col;
@@ -544,14 +570,13 @@ __device__ __forceinline__ void finish(const Params& p, int64_t row, int64_t col
         else
             store_block<false>(p.y + e, p.ys + e / 32, a);
     } else {
-        store_row(reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col, a,
-                  static_cast<int>(p.n - col < 32 ? p.n - col : 32), p.align);
+        store_rows(p, turn, row, col, a);
     }
 }
 
 template <int CG, bool SWIGLU>
-__device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, const Bars& bars, const WaitCtx& wc,
-                         int kAccCols) {
+__device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, uint32_t turn, const Bars& bars,
+                         const WaitCtx& wc, int kAccCols) {
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const bool shared_cols = 2 * p.width > kAccCols;
@@ -581,7 +606,7 @@ __device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, con
             load32(acc + 32 * at, a);
             if constexpr (SWIGLU) load32(acc + p.width / 2 + 32 * at, b);
             tc::tmem_wait_ld();
-            finish<SWIGLU>(p, row, n0 + 32 * at, a, b);
+            finish<SWIGLU>(p, turn, row, n0 + 32 * at, a, b);
         }
     }
 }
@@ -641,7 +666,7 @@ struct Exchange {
             }
         }
     }
-    __device__ void receive(int warp, int lane, int64_t t0, int64_t n0) const {
+    __device__ void receive(int warp, int lane, uint32_t turn, int64_t t0, int64_t n0) const {
         const int quarter = warp & 3, token = quarter * 32 + lane;
         if (t0 + quarter * 32 >= p.t) return;
         for (int c = u.part + (warp >> 2) * p.split; c < chunks; c += 2 * p.split) {
@@ -652,7 +677,7 @@ struct Exchange {
             tc::tmem_wait_ld();
             add(a, c, 0, token);
             if constexpr (SWIGLU) add(b, c, 1, token);
-            finish<SWIGLU>(p, t0 + token, n0 + 32 * c, a, b);
+            finish<SWIGLU>(p, turn, t0 + token, n0 + 32 * c, a, b);
         }
     }
 };
@@ -685,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Bars bars{base + plan.bars_at(p.ring, p.slots)};
     const uint32_t flag = bars.base + 8 * kNumBars, tslot = flag + 8;
+    const uint32_t turn = base + plan.turn_at(p.ring, p.slots) + (warp & 7) * kTurn;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (flag - raw));
     const WaitCtx wc{p.status, abort_flag};
     pdl_launch_dependents();
@@ -743,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kEpilogueWarps) {
         pdl_wait_previous();  // the previous kernel may still use what y is written over
         if (p.split == 1)
-            epilogue<CG, SWIGLU>(p, u, warp, lane, bars, wc, acc_cols(E2M1));
+            epilogue<CG, SWIGLU>(p, u, warp, lane, turn, bars, wc, acc_cols(E2M1));
         else
             summed = wait_all(bars.acc_full(0), 0, wc);  // a cluster has one tile
     } else if (warp == kCopyWarp) {
@@ -775,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp < kEpilogueWarps && summed) ex.send(warp, lane, t0);
         __syncwarp();
         cluster_sync_all();
-        if (warp < kEpilogueWarps && summed) ex.receive(warp, lane, t0, n0);
+        if (warp < kEpilogueWarps && summed) ex.receive(warp, lane, turn, t0, n0);
         __syncwarp();
     }
     tc::fence_before_sync();
@@ -872,16 +898,16 @@ struct Choice {
 };
 
 // Stages in the ring, and slots for the scales of as many and two groups more; false if not even two fit.
-bool fit(Choice& c, int rows_a, bool e2m1, int max_smem) {
+bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
     const Plan plan(c.width, c.cg, rows_a);
     auto slots_for = [&](int ring) {
         const int s = (ring * (e2m1 ? 2 : 1) + kGroupWords - 1) / kGroupWords + 2;
         return s < kMaxGroupSlots ? s : kMaxGroupSlots;
     };
     c.ring = 1;
-    while (c.ring < kMaxStages && plan.bytes(c.ring + 1, slots_for(c.ring + 1)) <= max_smem) ++c.ring;
+    while (c.ring < kMaxStages && plan.bytes(c.ring + 1, slots_for(c.ring + 1), turn) <= max_smem) ++c.ring;
     c.slots = slots_for(c.ring);
-    c.smem = plan.bytes(c.ring, c.slots);
+    c.smem = plan.bytes(c.ring, c.slots, turn);
     return c.ring > 1;
 }
 
@@ -894,7 +920,7 @@ bool fit(Choice& c, int rows_a, bool e2m1, int max_smem) {
 //   a launch           4.5 (a pair 5.5): first copies, last products, the stores
 //   a shared tile      1.7 and 20 KB a us for the sums that a CTA hands on
 // A part of k less per CTA only pays while every tile is on the GPU at once.
-Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, const Device& d) {
+Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn, const Device& d) {
     const int stages = static_cast<int>((k + (e2m1 ? 255 : 127)) / (e2m1 ? 256 : 128));
     const int groups = static_cast<int>((k / 128 + kGroupWords - 1) / kGroupWords);
     const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows;
@@ -912,7 +938,7 @@ Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, const Dev
                 const int longest = (groups + split - 1) / split * (kGroupWords / (e2m1 ? 2 : 1));
                 c.us = (split > 1 ? 1 : waves) * stage * (longest < stages ? longest : stages) + (cg == 1 ? 4.5f : 5.5f);
                 if (split > 1) c.us += 1.7f + rows_a * width * 4.f * (split - 1) / split / 20e3f;
-                if (c.us >= best.us || !fit(c, rows_a, e2m1, d.max_smem)) continue;
+                if (c.us >= best.us || !fit(c, rows_a, e2m1, turn, d.max_smem)) continue;
                 // The sums of the others have to fit the ring (chunks of 32 columns, of both halves where swiglu).
                 const int inbox = (outputs / 32 + split - 1) / split * (split - 1) * kRows * 128 * (swiglu ? 2 : 1);
                 if (inbox > c.ring * Plan(width, cg, rows_a).stage) continue;
@@ -938,10 +964,13 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
         Choice choice;
     };
     thread_local Kept kept[16];
-    const int kind = (a.e2m1 ? 2 : 0) + (a.swiglu ? 1 : 0);
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(2 * a.n);
+    const int align = rows_at % 32 == 0 ? 32 : rows_at % 16 == 0 ? 16 : 2;
+    const bool turn = !a.swiglu && align < 16;
+    const int kind = (a.e2m1 ? 2 : 0) + (a.swiglu ? 1 : 0) + (turn ? 4 : 0);
     Kept& slot = kept[(a.t * 31 + a.n * 7 + a.k / 128 + kind) & 15];
     if (slot.device != device || slot.t != a.t || slot.n != a.n || slot.k != a.k || slot.kind != kind)
-        slot = Kept{a.t, a.n, a.k, device, kind, choose(a.t, a.n, a.k, a.e2m1, a.swiglu, *device)};
+        slot = Kept{a.t, a.n, a.k, device, kind, choose(a.t, a.n, a.k, a.e2m1, a.swiglu, turn, *device)};
     const Choice& c = slot.choice;
     if (!c.cg) return cudaErrorInvalidValue;
     const int outputs = a.swiglu ? c.width / 2 : c.width, rows = kRows * c.cg;
@@ -959,8 +988,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     p.ring = c.ring;
     p.slots = c.slots;
     p.out_e2m1 = a.out_e2m1;
-    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(2 * a.n);
-    p.align = rows_at % 32 == 0 ? 32 : rows_at % 16 == 0 ? 16 : 2;
+    p.align = align;
     p.stages = static_cast<int>((a.k + (a.e2m1 ? 255 : 127)) / (a.e2m1 ? 256 : 128));
     const int64_t m_tiles = (a.t + rows - 1) / rows, n_tiles = (a.n + outputs - 1) / outputs;
     if (m_tiles * n_tiles >= (int64_t(1) << 27)) return cudaErrorInvalidValue;
