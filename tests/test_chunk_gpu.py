@@ -79,6 +79,8 @@ def test_quantize_strided_rows():
         whole = mx.quantize_mx(x[:, 64:320].contiguous(), form)
         part = mx.quantize_mx(x[:, 64:320], form)
         assert all(torch.equal(a.view(U8), b.view(U8)) for a, b in zip(whole, part))
+        narrow = mx.quantize_mx(x[:, 72:328], form)  # an offset of 16 bytes from where 32-byte loads may begin
+        assert torch.equal(narrow[1], mx.quantize_mx(x[:, 72:328].contiguous(), form)[1])
         every = mx.quantize_mx(x[::3], form)
         assert torch.equal(every[1], mx.quantize_mx(x[::3].contiguous(), form)[1])
 
