@@ -52,7 +52,8 @@ constexpr int kMaxGroupSlots = 6;
 constexpr int kMaxColumnSlots = 4;         // of TMEM columns with scales
 constexpr int kAhead = 2;                  // groups that a warp loads ahead
 constexpr int kTmemCols = 512;             // all of them, so the allocation begins at column 0
-constexpr int kTurn = 32 * 68;              // a warp's 32 x 32 outputs on their way to rows that are not aligned
+constexpr int kTurnRow = 80;               // 32 outputs of a token in shared memory, and a gap (banks)
+constexpr int kTurn = 32 * kTurnRow;       // a warp's
 constexpr int kImage = 512;                // scales of 128 rows and 128 values
 
 // Columns for two accumulators (of 256 each they share some); the rest holds
@@ -87,7 +88,7 @@ struct Bars {
 
 // Shared memory from a 1024-byte boundary: the ring (A then B of each stage),
 // the scale images of `slots` groups ([128 rows][word] each), barriers,
-// abort flag, TMEM base, room to turn unaligned outputs round.
+// abort flag, TMEM base, room to turn outputs round (if so wanted).
 struct Plan {
     int a, stage, sets, group;  // bytes of a stage's tokens, and of it all; sets of 128 rows with scales; bytes of a group's images
     // A product reads 128 rows of tokens. Where there are fewer in all, the rows behind them are whatever lies there (of
@@ -104,7 +105,7 @@ struct Plan {
         const int end = groups_at(ring) + slots * group, read = (ring - 1) * stage + kRows * kStageRow;
         return end > read ? end : read;
     }
-    __host__ __device__ int turn_at(int ring, int slots) const { return bars_at(ring, slots) + 8 * kNumBars + 16; }
+    __host__ __device__ int turn_at(int ring, int slots) const { return bars_at(ring, slots) + (8 * kNumBars + 31) / 16 * 16; }
     __host__ __device__ int bytes(int ring, int slots, bool turn) const {
         return turn_at(ring, slots) + (turn ? kEpilogueWarps * kTurn : 0) + 1024;
     }
@@ -493,12 +494,13 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
 }
 
 // The warp's 32 tokens x 32 outputs, lane i's of token `row`, `count` of them
-// wanted. Rows that begin at any even address go through shared memory: 64 bytes
-// of a token are written by 32 threads then (a thread's own 32 stores of 2 bytes
-// each touch a sector of their own).
+// wanted. Straight from the registers a store of the warp writes 32 bytes, whole
+// sectors, of 32 rows (through shared memory, 64 bytes of 8 rows, it was no
+// faster: 4,000 x 512 x 20,000 49 us against 47). Rows that begin at any even
+// address do go through shared memory: a thread's own 2-byte stores would each
+// touch a sector.
 __device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64_t row, int64_t col, const float (&v)[32]) {
     const int count = static_cast<int>(p.n - col < 32 ? p.n - col : 32), lane = threadIdx.x & 31;
-    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col;
     uint32_t w[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
@@ -507,6 +509,7 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64
     }
     if (p.align >= 16) {
         if (row >= p.t) return;
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y) + row * p.n + col;
         if (count < 32) {  // a multiple of 8
 #pragma unroll
             for (int q = 0; q < 3; ++q)
@@ -523,15 +526,16 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64
         return;
     }
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(turn + lane * 68 + 4 * q), "r"(w[q]) : "memory");
+    for (int q = 0; q < 4; ++q) sts128(turn + lane * kTurnRow + 16 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     __syncwarp();
-    const int rows = static_cast<int>(p.t - (row - lane) < 32 ? p.t - (row - lane) : 32);
-    uint16_t* to = reinterpret_cast<uint16_t*>(p.y) + (row - lane) * p.n + col + lane;
-    for (int i = 0; i < rows; ++i, to += p.n) {
+    const int64_t row0 = row - lane;
+    const int rows = static_cast<int>(p.t - row0 < 32 ? p.t - row0 : 32);
+    uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + row0 * p.n + col;
+    y += lane;
+    for (int r = 0; r < rows; ++r, y += p.n) {
         uint16_t h;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(turn + i * 68 + 2 * lane) : "memory");
-        if (lane < count) *to = h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(turn + r * kTurnRow + 2 * lane) : "memory");
+        if (lane < count) *y = h;
     }
     __syncwarp();
 }
@@ -592,22 +596,38 @@ __device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, uin
         tc::fence_after_sync();
         const uint32_t acc = lanes + ((i & 1) ? kAccCols - p.width : 0);
         const int64_t row = t0 + quarter * 32 + lane;
-        for (int c = 0; c <= chunks; ++c) {
-            if (c == early) {
-                tc::fence_before_sync();
-                __syncwarp();
-                const uint32_t freed = bars.acc_empty((i & 1) ^ (shared_cols ? 1 : 0));
-                if (lane == 0) arrive_at_first(freed, u);
-            }
-            if (c == chunks) break;
-            if ((c & 1) != half) continue;
-            const int at = (i & 1) || !shared_cols ? c : chunks - 1 - c;
+        // The accumulator is given back as soon as what the next tile needs of it is in registers: by then no chunk of
+        // this warp's before `early` is left. Two chunks at a time (one of both halves) keep loads and stores under way.
+        bool held = true;
+        auto give_back = [&](int next) {
+            if (!held || next < early) return;
+            held = false;
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_at_first(bars.acc_empty((i & 1) ^ (shared_cols ? 1 : 0)), u);
+        };
+        const bool down = shared_cols && !(i & 1);
+        give_back(half);
+        for (int c = half; c < chunks; c += SWIGLU ? 2 : 4) {
+            const int at = down ? chunks - 1 - c : c;
             float a[32], b[32];
             load32(acc + 32 * at, a);
-            if constexpr (SWIGLU) load32(acc + p.width / 2 + 32 * at, b);
-            tc::tmem_wait_ld();
-            finish<SWIGLU>(p, turn, row, n0 + 32 * at, a, b);
+            if constexpr (SWIGLU) {
+                load32(acc + p.width / 2 + 32 * at, b);
+                tc::tmem_wait_ld();
+                give_back(c + 2);
+                finish<SWIGLU>(p, turn, row, n0 + 32 * at, a, b);
+            } else {
+                const int then = down ? at - 2 : at + 2;
+                const bool two = c + 2 < chunks;
+                if (two) load32(acc + 32 * then, b);
+                tc::tmem_wait_ld();
+                give_back(c + 4);
+                finish<SWIGLU>(p, turn, row, n0 + 32 * at, a, a);
+                if (two) finish<SWIGLU>(p, turn, row, n0 + 32 * then, b, b);
+            }
         }
+        give_back(chunks);
     }
 }
 
