@@ -2,13 +2,17 @@
 projections, FFN and LM head next to the norms, rotary positions, paged
 attention and page bookkeeping that a step needs.
 
-    python examples/verify_step.py [--layers 4] [--steps 16] [--drafts 3]
+    python examples/verify_step.py [--layers 4] [--steps 16] [--drafts 3] [--prompt 50] [--prompt-chunk 8]
 
 Each step takes a sequence's last token and its drafts, runs them through the
 model as one chunk, accepts the drafts that agree with the model's own
 choices, and moves on: cache_accept keeps the accepted rows, cache_update cuts
 the sequence back and makes room for the next chunk. Weights are random; the
 drafts are the model's own earlier guesses for the positions ahead.
+
+The prompt goes in first, in chunks: of up to 8 tokens like a verify step, or
+with --prompt-chunk of more than 8 through the calls for many tokens
+(activations as microscaled 8-bit codes).
 """
 from __future__ import annotations
 
@@ -73,6 +77,25 @@ class Decoder:
         y, _ = mx.residual_norm(x, r, self.norm)
         return mx.linear(y, *self.head)
 
+    def prompt_chunk(self, tokens, cache, batch, form="e4m3"):
+        """The same layers for any number of new tokens (int64), whose K and V
+        go to the cache: activations as microscaled codes from the norms on.
+        Returns the bf16 rows [tokens, hidden] behind the last layer's
+        residual sum and norm."""
+        r = self.embed[tokens]
+        x = torch.zeros_like(r)
+        views = [cache.layer(i) for i in range(len(self.layers))]
+        ws = mx.attention_workspace(self.heads, views[0], batch)
+        for w, kv in zip(self.layers, views):
+            q, s, r = mx.residual_norm_mx(x, r, w["norm1"], format=form)
+            qkv = mx.linear_mx(q, s, *w["qkv"])
+            a = mx.attention(mx.rope_append(qkv, self.heads, self.inv_freq, kv, batch, factor=self.factor), kv, batch,
+                             workspace=ws)
+            a = mx.linear_mx(*mx.quantize_mx(a.view(len(tokens), -1), form), *w["out"])
+            q, s, r = mx.residual_norm_mx(a, r, w["norm2"], format=form)
+            x = mx.linear_mx(*mx.swiglu_mx(q, s, *w["up"], format=form), *w["down"])
+        return mx.residual_norm(x, r, self.norm)[0]
+
 
 class Sequences:
     """Sequences of a cache between steps: their pages and lengths."""
@@ -98,17 +121,18 @@ class Sequences:
         return mx.KVBatch(start, self.lens, self.table, tokens=n * new, max_q=new, max_seq=max_seq)
 
 
-def generate(model, prompt, steps, drafts=3, pages=256, page=16, dtype=BF16):
+def generate(model, prompt, steps, drafts=3, pages=256, page=16, dtype=BF16, prompt_chunk=8):
     """Greedy continuation of one prompt (a list of tokens) by verify steps of
     1 + drafts tokens; returns (tokens, accepted drafts per step)."""
     cache = model.new_cache(pages, page, dtype)
     seq = Sequences(cache, 1, pages)
     bound = pages * page
     dev = seq.table.device
-    for t in range(0, len(prompt) - 1, 8):  # the prompt in chunks of up to 8 (the FFN's limit)
-        part = prompt[t:min(t + 8, len(prompt) - 1)]
+    for t in range(0, len(prompt) - 1, prompt_chunk):  # a verify step's calls take up to 8 tokens (the FFN's limit)
+        part = prompt[t:min(t + prompt_chunk, len(prompt) - 1)]
         seq.room(len(part))
-        model.chunk(torch.tensor(part, device=dev), cache, seq.batch(len(part), bound))
+        run = model.chunk if prompt_chunk <= 8 else model.prompt_chunk
+        run(torch.tensor(part, device=dev), cache, seq.batch(len(part), bound))
     last, guess = torch.tensor([prompt[-1]], device=dev), torch.zeros(drafts, dtype=torch.int64, device=dev)
     out, taken = [], []
     path = torch.arange(1 + drafts, dtype=torch.int32, device=dev)[None]
@@ -133,18 +157,21 @@ def main():
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--drafts", type=int, default=3)
+    ap.add_argument("--prompt", type=int, default=50)
+    ap.add_argument("--prompt-chunk", type=int, default=8)
     a = ap.parse_args()
     model = Decoder(layers=a.layers)
-    prompt = [(i * 37 + 11) % model.vocab for i in range(50)]
-    generate(model, prompt, 2, a.drafts)
+    prompt = [(i * 37 + 11) % model.vocab for i in range(a.prompt)]
+    pages = (a.prompt + (a.steps + 2) * (1 + a.drafts)) // 16 + 64
+    generate(model, prompt, 2, a.drafts, pages, prompt_chunk=a.prompt_chunk)
     torch.cuda.synchronize()
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()
-    tokens, taken = generate(model, prompt, a.steps, a.drafts)
+    tokens, taken = generate(model, prompt, a.steps, a.drafts, pages, prompt_chunk=a.prompt_chunk)
     end.record()
     torch.cuda.synchronize()
     print(f"{len(tokens)} tokens in {a.steps} verify steps of {1 + a.drafts}, {sum(taken)} drafts accepted, "
-          f"{begin.elapsed_time(end) / a.steps:.2f} ms a step")
+          f"{begin.elapsed_time(end) / a.steps:.2f} ms a step, the prompt's {a.prompt} tokens included")
     print(tokens)
 
 

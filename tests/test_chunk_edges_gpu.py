@@ -2,6 +2,9 @@
 several streams at once, into the caller's memory, with sizes past 2^31, and
 waits that run out."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +15,7 @@ from step_cases import check, gen, randn
 
 pytestmark = pytest.mark.gpu
 BF16, U8 = torch.bfloat16, torch.uint8
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def bits(t):
@@ -231,3 +235,40 @@ def test_waits_run_out(withhold_lib, t, n, k, form):
     ref, mag = product(x, w)
     check(y, ref, ref.abs() * 2.0 ** -8 + sum_bound(k, mag), "afterwards")
     assert values(*w).isfinite().all()
+
+
+# ---------------------------------------------------------------- example
+@pytest.fixture(scope="module")
+def ex():
+    lib()
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import verify_step
+    return verify_step
+
+
+@pytest.mark.parametrize("form", ["e4m3", "e2m1"])
+def test_prompt_in_chunks(ex, form):
+    """A prompt in one chunk, twice, and in three: the same bits, and what eight
+    quantisations in a row (two layers) may make of other orders of the sums: each
+    rounds by at most 2^-4 (2^-2) of its input."""
+    model = ex.Decoder(layers=2, hidden=512, heads=4, kv_heads=2, inter=512, vocab=512)
+    tokens = torch.arange(300, device="cuda") * 11 % 512
+    rows = []
+    for sizes in ([300], [300], [100, 37, 163]):
+        seq, out, at = ex.Sequences(model.new_cache(64), 1, 32), [], 0
+        for n in sizes:
+            seq.room(n)
+            out.append(model.prompt_chunk(tokens[at:at + n], seq.cache, seq.batch(n, 512), form))
+            at += n
+        rows.append(torch.cat(out))
+        assert int(seq.lens) == 300
+    assert torch.equal(bits(rows[0]), bits(rows[1]))
+    a, b = rows[0].double(), rows[2].double()
+    assert a.isfinite().all() and (a - b).norm() < 8 * (2 ** -4 if form == "e4m3" else 2 ** -2) * a.norm()
+
+
+def test_example_with_a_long_prompt():
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "verify_step.py"), "--layers", "1", "--steps", "3",
+                        "--prompt", "700", "--prompt-chunk", "256"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "verify steps" in r.stdout
