@@ -338,6 +338,8 @@ __device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, in
         if (tile < p.tiles) skip();
         r.next(p.slots);
     }
+    if (tile < p.tiles) rows_of(tile);
+    turned = false;
     if (set == 0) pdl_wait_previous();  // the tokens may come from the previous kernel, weights do not
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) load(v[d]);
