@@ -34,7 +34,17 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 // 2^(127 - s): what a block's values are multiplied with (exact).
 __device__ __forceinline__ float inverse_scale(uint32_t s) { return exp2_int(127 - static_cast<int>(s)); }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Bits of the largest magnitude of N values (an even number); of a NaN's if there
+// is one. Three-way maxima: half an instruction a value.
+template <int N>
+__device__ __forceinline__ uint32_t largest(const float* v) {
+    float m = fabsf(v[0]);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v[1])));
+#pragma unroll
+    for (int i = 2; i < N; i += 2)
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
+    return __float_as_uint(m);
+}
 
 // N values, already in units of their scale, as N / 4 words of E4M3 or N / 8 of E2M1.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -59,10 +69,15 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
 // codes are NaN too; E2M1 has none.
 template <bool E2M1, int N>
 __device__ __forceinline__ void encode(const float* v, uint32_t s, uint32_t (&out)[E2M1 ? N / 8 : N / 4]) {
-    const float f = s == kNanScale ? 0.f : inverse_scale(s);
+    const float f = inverse_scale(s);
+    const uint64_t f2 = f32x2_pack(f, f);
     float z[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = v[i] * f;
+    for (int i = 0; i < N; i += 2) {
+        const float2 w = f32x2_unpack(f32x2_mul(f32x2_pack(v[i], v[i + 1]), f2));
+        z[i] = w.x;
+        z[i + 1] = w.y;
+    }
     if constexpr (E2M1) {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) out[i] = s == kNanScale ? 0u : e2m1x8(z + 8 * i);
@@ -73,8 +88,25 @@ __device__ __forceinline__ void encode(const float* v, uint32_t s, uint32_t (&ou
     }
 }
 
-// SiLU(a) * b. exp(-a) may overflow to infinity: a / inf is the right 0.
-__device__ __forceinline__ float swiglu(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
+// z[i] = SiLU(z[i]) * up[i] = z / (1 + 2^(-z log2 e)) * up in fp32, two at a time.
+// The power may overflow to infinity: its reciprocal is the right 0.
+template <int N>
+__device__ __forceinline__ void swiglu(float* z, const float* up) {
+    const uint64_t minus_log2e = f32x2_pack(-1.44269504f, -1.44269504f), one = f32x2_pack(1.f, 1.f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint64_t a = f32x2_pack(z[i], z[i + 1]);
+        float2 e = f32x2_unpack(f32x2_mul(a, minus_log2e));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        float2 d = f32x2_unpack(f32x2_fma(f32x2_pack(e.x, e.y), one, one));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.y));
+        const float2 h = f32x2_unpack(f32x2_mul(f32x2_mul(a, f32x2_pack(d.x, d.y)), f32x2_pack(up[i], up[i + 1])));
+        z[i] = h.x;
+        z[i + 1] = h.y;
+    }
+}
 
 }  // namespace mx
 }  // namespace mxfp4

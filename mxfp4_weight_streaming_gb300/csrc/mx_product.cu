@@ -544,10 +544,7 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64
 
 template <bool OUT_E2M1>
 __device__ __forceinline__ void store_block(uint8_t* q, uint8_t* s, const float (&h)[32]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) top = max(top, mx::abs_bits(h[j]));
-    const uint32_t b = mx::scale_byte<OUT_E2M1>(top);
+    const uint32_t b = mx::scale_byte<OUT_E2M1>(mx::largest<32>(h));
     uint32_t w[OUT_E2M1 ? 4 : 8];
     mx::encode<OUT_E2M1, 32>(h, b, w);
     if constexpr (OUT_E2M1)
@@ -568,8 +565,7 @@ __device__ __forceinline__ void finish(const Params& p, uint32_t turn, int64_t r
     if (col >= p.n || row - (threadIdx.x & 31) >= p.t) return;  // none of the warp's tokens
     if constexpr (SWIGLU) {
         if (row >= p.t) return;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) a[j] = mx::swiglu(a[j], b[j]);
+        mx::swiglu<32>(a, b);
         const int64_t e = row * p.n + col;
         if (p.out_e2m1)
             store_block<true>(p.y + e / 2, p.ys + e / 32, a);

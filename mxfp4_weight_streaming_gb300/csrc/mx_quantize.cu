@@ -65,12 +65,9 @@ __global__ void __launch_bounds__(256, 8) mx_quantize_kernel(QuantizeParams p) {
             float up[16];
             unpack8(b.v[0], *reinterpret_cast<float(*)[8]>(up));
             unpack8(b.v[1], *reinterpret_cast<float(*)[8]>(up + 8));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = mx::swiglu(z[j], up[j]);
+            mx::swiglu<16>(z, up);
         }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = max(top, mx::abs_bits(z[j]));
+        uint32_t top = mx::largest<16>(z);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         const uint32_t s = mx::scale_byte<E2M1>(top);
         uint32_t w[E2M1 ? 2 : 4];

@@ -88,9 +88,7 @@ enum { kBf16, kE4M3, kE2M1 };
 // block of 32 (n % 32 == 0, so none straddles the row's end).
 template <bool E2M1>
 __device__ __forceinline__ void store_codes(const NormParams& p, int64_t row, int at, const float (&v)[8]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, mx::abs_bits(v[j]));
+    uint32_t top = mx::largest<8>(v);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t s = mx::scale_byte<E2M1>(top);
