@@ -8,10 +8,20 @@
 // instruction). Sums are fp32 in TMEM; y is rounded once, h not at all before
 // its codes.
 //
-// A tile is 128 tokens x `width` weight rows (width: a multiple of 32 up to
-// 256; for the gated form the first half are gate rows, the second the up rows
-// of the same outputs, so a thread finds both of its token in one TMEM lane).
-// A stage is 128 bytes of every row: 128 values of k, or 256 in E2M1.
+// A tile is 128 tokens (a pair of CTAs: 256) x `width` weight rows (width: a
+// multiple of 32 up to 256; for the gated form the first half are gate rows, the
+// second the up rows of the same outputs, so a thread finds both of its token in
+// one TMEM lane). A stage is 128 bytes of every row: 128 values of k, or 256 in
+// E2M1. Where there are few tiles, the CTAs (or pairs) of a cluster take a part of
+// k each and hand their sums on through distributed shared memory.
+//
+// What bounds a stage: its products (512 cycles at 128 x 256 per SM in E4M3, and no
+// less than 119 each however narrow), and shared memory, where every byte is
+// written once and read once at 128 bytes a cycle: 512 cycles for a pair's 256-wide
+// tile, 768 for a lone CTA's. Measured: 4,096 tokens x 7,168 x 2 x 18,432 gated 590
+// to 630 us (3.4 to 3.7 PFLOP/s, under the power cap), 4,096 x 18,432 x 7,168 in
+// E2M1 148 us (7.3), 512 x 7,168 x 9,216 26 us, 61 x 7,168 x 129,280 90 us (5.6
+// TB/s), 16 x 7,168 x 7,168 13 us, of which 8 are the call's beginning and end.
 //
 // One CTA per SM walks over tiles, warp-specialised:
 //   0-7    epilogue: warp w reads the lanes (tokens) 32 (w % 4) .. of the
@@ -19,11 +29,11 @@
 //   8      copies codes (TMA) into a ring of stages
 //   9      issues the scales' copies into TMEM and the products
 //   10-15  scales: 128 tokens, and weight rows 0-127 and 128-255 of the tile,
-//          two warps each. A lane holds rows l, l + 32, l + 64, l + 96 and writes the word of
-//          128 values of each as one 16-byte line, the layout that the copy
-//          into TMEM wants; the words of the next stages are loaded ahead
+//          two warps each. A lane holds rows l, l + 32, l + 64, l + 96 and writes
+//          the word of 128 values of each as one 16-byte line, the layout that the
+//          copy into TMEM wants; the words of the next stages are loaded ahead
 // Two accumulators alternate, so the next tile's products run under the
-// epilogue.
+// epilogue. Every wait is bounded (device_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -261,10 +271,10 @@ struct Copier {
 };
 
 // ---------------------------------------------------------------- scales
-// Warp `set` of the scale warps: set 0 tokens, 1 and 2 weight rows.
+// Set 0: tokens, 1 and 2: weight rows. Warp `turn` (0, 1) of the set takes every second group.
 template <int CG, bool SWIGLU>
-__device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, int set, int turn, int lane, uint32_t base, const Bars& bars,
-                            const WaitCtx& wc) {
+__device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, int set, int turn, int lane, uint32_t base,
+                            const Bars& bars, const WaitCtx& wc) {
     const int64_t pitch = p.k / 32;
     const int words = static_cast<int>(p.k / 128);
     const uint8_t* array = set == 0 ? p.xs : p.ws;
@@ -294,7 +304,7 @@ __device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, in
             row[q] = valid ? array + at * pitch : nullptr;
         }
     };
-    // The set's other warp takes every second group, and each has its next kAhead groups on their way in registers: a
+    // Each warp has its next kAhead groups on their way in registers: a
     // group of 512 values is multiplied in 0.3 us and more, its loads from HBM take over 1 us, and getting it into place
     // some 1,000 cycles.
     uint4 v[kAhead][4];
@@ -532,8 +542,7 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t turn, int64
     __syncwarp();
     const int64_t row0 = row - lane;
     const int rows = static_cast<int>(p.t - row0 < 32 ? p.t - row0 : 32);
-    uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + row0 * p.n + col;
-    y += lane;
+    uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + row0 * p.n + col + lane;
     for (int r = 0; r < rows; ++r, y += p.n) {
         uint16_t h;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(turn + r * kTurnRow + 2 * lane) : "memory");
@@ -631,15 +640,14 @@ __device__ void epilogue(const Params& p, const Unit& u, int warp, int lane, uin
 
 // The end of a tile whose k is split over a cluster: chunk c of the columns
 // belongs to part c % split, whose CTA takes the others' sums of it into its
-// ring (free by then) and adds them in the parts' order, so results do not
-// depend on who comes first.
+// ring (free by then) and adds them to its own in the parts' order, so results
+// do not depend on who comes first.
 //   box (chunk c / split, sender): [8 or 2 x 8 pieces of 4 fp32][128 tokens], so
 //   that a warp's store is 512 bytes in a row (stores of 16 bytes 128 apart
 //   took 3 us longer a tile)
 template <bool SWIGLU>
 struct Exchange {
     static constexpr int kHalves = SWIGLU ? 2 : 1;
-    static constexpr int kBox = kRows * 128 * kHalves;
     const Params& p;
     const Unit& u;
     uint32_t base;
@@ -944,7 +952,7 @@ Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn
     const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows;
     Choice best{};
     best.us = 1e30f;
-    for (int cg = 1; cg <= (t > kRows ? 2 : 1); ++cg) {
+    for (int cg = 1; cg <= (t > kRows && d.clusters[2] > 0 ? 2 : 1); ++cg) {
         for (int width = swiglu ? 64 : 32; width <= 256; width += swiglu ? 64 : 32) {
             const int outputs = swiglu ? width / 2 : width;
             const float stage = cg == 1 ? 0.14f + 0.0008f * width : 0.13f + 0.0007f * width;

@@ -11,6 +11,9 @@
 // Everything is fp32 until the one rounding of each output; y is the norm of
 // the unrounded r.
 //
+// y may leave as microscaled codes (mx_common.cuh) instead: 4,096 tokens of 7,168
+// with post norm and a gate per token, 265 MB, take 50 us, 77 % of the copy rate.
+//
 // Bound by HBM: 4,096 tokens of 7,168 with a gate per token, 294 MB, take 51
 // us, 84 % of the copy rate (82 us with a block per row and no loads ahead);
 // 4 tokens take 3.1 us, a launch.
