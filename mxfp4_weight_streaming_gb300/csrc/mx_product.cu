@@ -75,7 +75,8 @@ struct Params {
     uint8_t *y, *ys;
     unsigned* status;
     int64_t t, n, k;
-    int m_tiles, tiles, width, stages;     // stages: of the whole k
+    int m_tiles, n_tiles, tiles, width;
+    int stages;                            // of the whole k
     int ring, slots;                       // stages and groups of scales in shared memory
     int split;                             // CTAs (or pairs) of a cluster that share a tile, each a part of k
     int rows_a, rows_b;                    // rows of a copied box
@@ -83,6 +84,7 @@ struct Params {
     int align;                             // bytes that every row of y begins at a multiple of (32, 16 or 2)
 };
 
+// Barriers, then the abort flag and the TMEM base.
 constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxGroupSlots + 4 + kMaxColumnSlots + 1;
 struct Bars {
     uint32_t base;
@@ -94,11 +96,23 @@ struct Bars {
     __device__ uint32_t acc_empty(int b) const { return base + 8 * (2 * kMaxStages + 2 * kMaxGroupSlots + 2 + b); }
     __device__ uint32_t columns_free(int s) const { return base + 8 * (2 * kMaxStages + 2 * kMaxGroupSlots + 4 + s); }
     __device__ uint32_t drain() const { return base + 8 * (kNumBars - 1); }
+    __device__ uint32_t abort_flag() const { return base + 8 * kNumBars; }
+    __device__ uint32_t tmem_base() const { return base + 8 * kNumBars + 8; }
+    // All of them, by the lanes of a warp (one thread alone takes 0.6 us).
+    __device__ void init(int lane, uint32_t scales, uint32_t epilogue) const {
+        for (int i = lane; i < kNumBars; i += 32) {
+            const int g = i - 2 * kMaxStages, b = g - 2 * kMaxGroupSlots;
+            mbar_init(base + 8 * i, g >= 0 && g < kMaxGroupSlots ? scales : b == 2 || b == 3 ? epilogue : 1u);
+        }
+        fence_barrier_init();
+    }
 };
+constexpr int kBarBytes = 1024;
+static_assert(8 * kNumBars + 16 <= kBarBytes, "barriers, flag and TMEM base");
 
-// Shared memory from a 1024-byte boundary: the ring (A then B of each stage),
-// the scale images of `slots` groups ([128 rows][word] each), barriers,
-// abort flag, TMEM base, room to turn outputs round (if so wanted).
+// Shared memory from a 1024-byte boundary: barriers, the ring (A then B of each
+// stage), the scale images of `slots` groups ([128 rows][word] each), room to
+// turn outputs round (if so wanted).
 struct Plan {
     int a, stage, sets, group;  // bytes of a stage's tokens, and of it all; sets of 128 rows with scales; bytes of a group's images
     // A product reads 128 rows of tokens. Where there are fewer in all, the rows behind them are whatever lies there (of
@@ -110,14 +124,13 @@ struct Plan {
         sets = 1 + (width + 127) / 128;
         group = sets * kGroupWords * kImage;
     }
-    __host__ __device__ int groups_at(int ring) const { return ring * stage; }
-    __host__ __device__ int bars_at(int ring, int slots) const {
+    __host__ __device__ int groups_at(int ring) const { return ring * stage; }  // from the ring's begin
+    __host__ __device__ int turn_at(int ring, int slots) const {
         const int end = groups_at(ring) + slots * group, read = (ring - 1) * stage + kRows * kStageRow;
         return end > read ? end : read;
     }
-    __host__ __device__ int turn_at(int ring, int slots) const { return bars_at(ring, slots) + (8 * kNumBars + 31) / 16 * 16; }
     __host__ __device__ int bytes(int ring, int slots, bool turn) const {
-        return turn_at(ring, slots) + (turn ? kEpilogueWarps * kTurn : 0) + 1024;
+        return kBarBytes + turn_at(ring, slots) + (turn ? kEpilogueWarps * kTurn : 0) + 1024;
     }
 };
 
@@ -168,8 +181,7 @@ __device__ __forceinline__ void arrive_at_first(uint32_t bar, const Unit& u) {
 template <int CG, bool SWIGLU>
 __device__ __forceinline__ void place(const Params& p, int tile, int64_t& t0, int64_t& n0) {
     constexpr int kGroup = 16;
-    const int n_tiles = p.tiles / p.m_tiles;
-    const int group = tile / (kGroup * n_tiles), in = tile - group * kGroup * n_tiles;
+    const int group = tile / (kGroup * p.n_tiles), in = tile - group * kGroup * p.n_tiles;
     const int high = min(kGroup, p.m_tiles - group * kGroup);
     const int nt = in / high;
     t0 = static_cast<int64_t>(group * kGroup + in - nt * high) * (CG * kRows);
@@ -225,15 +237,17 @@ struct Copier {
     __device__ __forceinline__ void tokens(int slot, int k) const {
         codes(base + slot * plan.stage, amap, k, t0 + u.rank * kRows, full(slot));
     }
+    // Test-only builds: the first cluster's first CTA never gets its first stage.
+    __device__ __forceinline__ bool withheld(int j) const { return u.first == 0 && withhold_stage(static_cast<uint32_t>(j)); }
     // The weights of the ring's first round. They do not wait for the previous kernel of the stream.
     __device__ __forceinline__ void begin() const {
         for (int j = 0; j < first; ++j)
-            if (!withhold_stage(static_cast<uint32_t>(j))) weights(j, u.stage0 + j);
+            if (!withheld(j)) weights(j, u.stage0 + j);
     }
     __device__ __forceinline__ void run(const WaitCtx& wc) {
         pdl_wait_previous();  // it may still write the tokens
         for (int j = 0; j < first; ++j)
-            if (!withhold_stage(static_cast<uint32_t>(j))) tokens(j, u.stage0 + j);
+            if (!withheld(j)) tokens(j, u.stage0 + j);
         Ring r;
         int issued = 0;
         bool ok = true;
@@ -273,14 +287,42 @@ struct Copier {
 // ---------------------------------------------------------------- scales
 // Set 0: tokens, 1 and 2: weight rows. Warp `turn` (0, 1) of the set takes every second group.
 template <int CG, bool SWIGLU>
-__device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, int set, int turn, int lane, uint32_t base,
-                            const Bars& bars, const WaitCtx& wc) {
-    const int64_t pitch = p.k / 32;
-    const int words = static_cast<int>(p.k / 128);
-    const uint8_t* array = set == 0 ? p.xs : p.ws;
-    const bool wide = pitch % 16 == 0 && (reinterpret_cast<uintptr_t>(array) & 15) == 0;
-    const uint8_t* row[4];
-    auto rows_of = [&](int tile) {
+struct Scales {
+    const Params& p;
+    const Plan& plan;
+    const Unit& u;
+    int set, lane;
+    uint32_t ring;
+    const Bars& bars;
+    const uint8_t* array;
+    bool wide;              // 16-byte loads
+    const uint8_t* row[4];  // of the tile that is being loaded
+    // Each warp has its next kAhead groups on their way in registers: a group of 512 values is multiplied in 0.3 us and
+    // more, its loads from HBM take over 1 us, and getting it into place some 1,000 cycles.
+    uint4 v[kAhead][4];
+    int tile, g;            // the next group to load
+    bool turned;            // the rows are not this tile's yet
+    int64_t left;           // groups of this CTA from the next one on
+    Ring r;
+
+    __device__ __forceinline__ Scales(const Params& p_, const Plan& plan_, const Unit& u_, int set_, int turn, int lane_,
+                                      uint32_t ring_, const Bars& bars_)
+        : p(p_), plan(plan_), u(u_), set(set_), lane(lane_), ring(ring_), bars(bars_) {
+        array = set == 0 ? p.xs : p.ws;
+        wide = p.k % 512 == 0 && (reinterpret_cast<uintptr_t>(array) & 15) == 0;
+        tile = u.first;
+        g = u.group0;
+        left = tile < p.tiles ? static_cast<int64_t>((p.tiles - tile + u.step - 1) / u.step) * u.groups : 0;
+        if (turn) {
+            --left;
+            if (tile < p.tiles) skip();
+            r.next(p.slots);
+        }
+        if (tile < p.tiles) rows_of();
+        turned = false;
+    }
+    __device__ __forceinline__ void rows_of() {
+        const int64_t pitch = p.k / 32;
         int64_t t0, n0;
         place<CG, SWIGLU>(p, tile, t0, n0);
         t0 += u.rank * kRows;
@@ -303,23 +345,17 @@ __device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, in
             }
             row[q] = valid ? array + at * pitch : nullptr;
         }
-    };
-    // Each warp has its next kAhead groups on their way in registers: a
-    // group of 512 values is multiplied in 0.3 us and more, its loads from HBM take over 1 us, and getting it into place
-    // some 1,000 cycles.
-    uint4 v[kAhead][4];
-    int tile = u.first, g = u.group0;  // the next group to load
-    bool turned = true;                // the rows are not this tile's yet
-    auto skip = [&] {
+    }
+    __device__ __forceinline__ void skip() {
         if (++g == u.group0 + u.groups) {
             g = u.group0;
             tile = u.step < p.tiles - tile ? tile + u.step : p.tiles;
             turned = true;
         }
-    };
-    auto load = [&](uint4 (&to)[4]) {
+    }
+    __device__ __forceinline__ void load(uint4 (&to)[4]) {
         if (tile >= p.tiles) return;
-        if (turned) rows_of(tile);
+        if (turned) rows_of();
         turned = false;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -330,50 +366,44 @@ __device__ void copy_scales(const Params& p, const Plan& plan, const Unit& u, in
                 to[q] = __ldcg(reinterpret_cast<const uint4*>(row[q]) + g);
             } else {
                 const uint32_t* s = reinterpret_cast<const uint32_t*>(row[q]) + kGroupWords * g;
-                const int left = words - kGroupWords * g;
+                const int words = static_cast<int>(p.k / 128) - kGroupWords * g;
                 to[q].x = __ldcg(s);
-                if (left > 1) to[q].y = __ldcg(s + 1);
-                if (left > 2) to[q].z = __ldcg(s + 2);
-                if (left > 3) to[q].w = __ldcg(s + 3);
+                if (words > 1) to[q].y = __ldcg(s + 1);
+                if (words > 2) to[q].z = __ldcg(s + 2);
+                if (words > 3) to[q].w = __ldcg(s + 3);
             }
         }
         skip();
         if (tile < p.tiles) skip();
-    };
-    // This CTA's groups in all, and this warp's first.
-    int64_t left = u.first < p.tiles ? static_cast<int64_t>((p.tiles - u.first + u.step - 1) / u.step) * u.groups : 0;
-    Ring r;
-    if (turn) {
-        --left;
-        if (tile < p.tiles) skip();
-        r.next(p.slots);
     }
-    if (tile < p.tiles) rows_of(tile);
-    turned = false;
-    if (set == 0) pdl_wait_previous();  // the tokens may come from the previous kernel, weights do not
+    // The first groups: of weights at once, of tokens when the previous kernel, which may write them, has ended.
+    __device__ __forceinline__ void begin() {
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) load(v[d]);
-    while (left > 0) {
+        for (int d = 0; d < kAhead; ++d) load(v[d]);
+    }
+    __device__ __forceinline__ void run(const WaitCtx& wc) {
+        while (left > 0) {
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-            if (left <= 0) break;
-            left -= 2;
-            if (!wait_all(bars.scales_empty(r.slot), r.phase ^ 1u, wc)) return;
-            const uint4(&w)[4] = v[d];
-            const uint32_t at = base + plan.groups_at(p.ring) + r.slot * plan.group + set * kGroupWords * kImage + lane * 16;
-            sts128(at, w[0].x, w[1].x, w[2].x, w[3].x);
-            sts128(at + kImage, w[0].y, w[1].y, w[2].y, w[3].y);
-            sts128(at + 2 * kImage, w[0].z, w[1].z, w[2].z, w[3].z);
-            sts128(at + 3 * kImage, w[0].w, w[1].w, w[2].w, w[3].w);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) arrive_at_first(bars.scales_full(r.slot), u);
-            load(v[d]);
-            r.next(p.slots);
-            r.next(p.slots);
+            for (int d = 0; d < kAhead; ++d) {
+                if (left <= 0) break;
+                left -= 2;
+                if (!wait_all(bars.scales_empty(r.slot), r.phase ^ 1u, wc)) return;
+                const uint4(&w)[4] = v[d];
+                const uint32_t at = ring + plan.groups_at(p.ring) + r.slot * plan.group + set * kGroupWords * kImage + lane * 16;
+                sts128(at, w[0].x, w[1].x, w[2].x, w[3].x);
+                sts128(at + kImage, w[0].y, w[1].y, w[2].y, w[3].y);
+                sts128(at + 2 * kImage, w[0].z, w[1].z, w[2].z, w[3].z);
+                sts128(at + 3 * kImage, w[0].w, w[1].w, w[2].w, w[3].w);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) arrive_at_first(bars.scales_full(r.slot), u);
+                load(v[d]);
+                r.next(p.slots);
+                r.next(p.slots);
+            }
         }
     }
-}
+};
 
 // -------------------------------------------------------------- products
 // The instructions of one CTA or of a pair.
@@ -715,17 +745,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const Plan plan(p.width, CG, p.rows_a);
+    const Bars bars{(raw + 1023u) & ~1023u};
+    const uint32_t base = bars.base + kBarBytes;  // of the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (bars.abort_flag() - raw));
+    const WaitCtx wc{p.status, abort_flag};
+    const Plan plan(p.width, CG, p.rows_a);
+    pdl_launch_dependents();
+    // What takes long is begun first: TMEM by the issuing warp, barriers by the copying one.
+    if (warp == kMmaWarp) {
+        if constexpr (CG == 1) {
+            tc::tmem_alloc(bars.tmem_base(), kTmemCols);
+            tc::tmem_relinquish();
+        } else {
+            tc::tmem_alloc_pair(bars.tmem_base(), kTmemCols);
+            tc::tmem_relinquish_pair();
+        }
+    }
+    const bool alone = CG == 1 && p.split == 1;
+    if (warp == kCopyWarp) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&bmap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&amap) : "memory");
+            *abort_flag = 0;
+        }
+        bars.init(lane, static_cast<uint32_t>(CG * plan.sets), CG * kEpilogueWarps);
+        __syncwarp();
+        // It goes on to the first copies while the others wait for barriers and TMEM.
+        if (alone)
+            asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
     Unit u;
     {
         constexpr int kGroupStages = kGroupWords / (E2M1 ? 2 : 1);
-        const int cluster = CG * p.split;
-        const uint32_t in = blockIdx.x % cluster;
+        const uint32_t in = blockIdx.x;  // a cluster is a row of the grid
         const int groups = (p.stages + kGroupStages - 1) / kGroupStages;
-        u.first = static_cast<int>(blockIdx.x) / cluster;
-        u.step = static_cast<int>(gridDim.x) / cluster;
+        u.first = blockIdx.y;
+        u.step = gridDim.y;
         u.part = static_cast<int>(in) / CG;
         u.rank = in % CG;
         u.leader = in - u.rank;
@@ -734,76 +792,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.stage0 = u.group0 * kGroupStages;
         u.stages = min(u.groups * kGroupStages, p.stages - u.stage0);
     }
-    const Bars bars{base + plan.bars_at(p.ring, p.slots)};
-    const uint32_t flag = bars.base + 8 * kNumBars, tslot = flag + 8;
-    const uint32_t turn = base + plan.turn_at(p.ring, p.slots) + (warp & 7) * kTurn;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (flag - raw));
-    const WaitCtx wc{p.status, abort_flag};
-    pdl_launch_dependents();
-    if (warp == kCopyWarp && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&bmap) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&amap) : "memory");
-    }
-    if (warp == kMmaWarp) {
-        if constexpr (CG == 1) {
-            tc::tmem_alloc(tslot, kTmemCols);
-            tc::tmem_relinquish();
-        } else {
-            tc::tmem_alloc_pair(tslot, kTmemCols);
-            tc::tmem_relinquish_pair();
-        }
-    }
-    // Barriers are the copying warp's, which goes on to the first copies while the others wait for them and for TMEM.
-    const bool alone = CG == 1 && p.split == 1;
-    Copier<CG, E2M1, SWIGLU> copier(p, plan, u, &amap, &bmap, base, bars);
-    if (warp == kCopyWarp) {
-        if (lane == 0) {
-            for (int s = 0; s < p.ring; ++s) {
-                mbar_init(bars.full(s), 1);
-                mbar_init(bars.empty(s), 1);
-            }
-            for (int g = 0; g < p.slots; ++g) {
-                mbar_init(bars.scales_full(g), static_cast<uint32_t>(CG * plan.sets));
-                mbar_init(bars.scales_empty(g), 1);
-            }
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(bars.acc_full(b), 1);
-                mbar_init(bars.acc_empty(b), CG * kEpilogueWarps);
-            }
-            for (int s = 0; s < kMaxColumnSlots; ++s) mbar_init(bars.columns_free(s), 1);
-            mbar_init(bars.drain(), 1);
-            *abort_flag = 0;
-            fence_barrier_init();
-        }
-        __syncwarp();
-        if (alone)
-            asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-        else
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        if (lane == 0 && u.rank == 0) copier.begin();  // on barriers of its own
-        __syncwarp();
-        if (!alone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    } else {
+    auto ready = [&] {
         tc::fence_before_sync();
         if (alone)
             asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
         else
             cluster_sync_all();
         tc::fence_after_sync();
-    }
+    };
     bool summed = true;
     if (warp < kEpilogueWarps) {
+        ready();
         pdl_wait_previous();  // the previous kernel may still use what y is written over
+        const uint32_t turn = base + plan.turn_at(p.ring, p.slots) + warp * kTurn;
         if (p.split == 1)
             epilogue<CG, SWIGLU>(p, u, warp, lane, turn, bars, wc, acc_cols(E2M1));
         else
             summed = wait_all(bars.acc_full(0), 0, wc);  // a cluster has one tile
     } else if (warp == kCopyWarp) {
+        Copier<CG, E2M1, SWIGLU> copier(p, plan, u, &amap, &bmap, base, bars);
+        if (lane == 0 && u.rank == 0) copier.begin();  // on barriers of its own
+        __syncwarp();
+        if (!alone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (lane == 0) {
             if (u.rank != 0) copier.begin();
             copier.run(wc);
         }
     } else if (warp == kMmaWarp) {
+        ready();
         if (u.rank == 0 && !issue_products<CG, E2M1>(p, plan, u, base, bars, wc)) {
             // Products issued so far may still read shared memory and write TMEM: waited for, bounded.
             if (lane == 0) {
@@ -813,8 +829,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(bars.drain(), 0, own);
             }
         }
-    } else if ((warp - kScaleWarp) % 3 < plan.sets) {
-        copy_scales<CG, SWIGLU>(p, plan, u, (warp - kScaleWarp) % 3, (warp - kScaleWarp) / 3, lane, base, bars, wc);
+    } else {
+        const int set = (warp - kScaleWarp) % 3;
+        if (set < plan.sets) {
+            Scales<CG, SWIGLU> scales(p, plan, u, set, (warp - kScaleWarp) / 3, lane, base, bars);
+            if (alone) {
+                ready();
+                if (set == 0) pdl_wait_previous();
+                scales.begin();
+            } else {
+                // The cluster's barrier would wait for loads under way.
+                asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+                if (set == 0) pdl_wait_previous();
+                scales.begin();
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            }
+            scales.run(wc);
+        } else {
+            ready();
+        }
     }
     __syncwarp();
     if (p.split > 1) {
@@ -827,7 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp < kEpilogueWarps && summed) ex.send(warp, lane, t0);
         __syncwarp();
         cluster_sync_all();
-        if (warp < kEpilogueWarps && summed) ex.receive(warp, lane, turn, t0, n0);
+        if (warp < kEpilogueWarps && summed)
+            ex.receive(warp, lane, base + plan.turn_at(p.ring, p.slots) + warp * kTurn, t0, n0);
         __syncwarp();
     }
     tc::fence_before_sync();
@@ -852,9 +886,9 @@ cudaError_t configure(int smem) {
 }
 
 template <int CG, bool E2M1, bool SWIGLU>
-cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, int grid,
+cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p, int smem, dim3 grid,
                    cudaStream_t stream) {
-    PdlLaunch l(dim3(grid), dim3(kThreads), smem, stream);
+    PdlLaunch l(grid, dim3(kThreads), smem, stream);
     if (CG * p.split > 1) {
         cudaLaunchAttribute& cluster = l.attr[l.cfg.numAttrs++];
         cluster.id = cudaLaunchAttributeClusterDimension;
@@ -866,7 +900,7 @@ cudaError_t launch(const CUtensorMap& amap, const CUtensorMap& bmap, const Param
 
 template <int CG>
 cudaError_t launch_any(bool e2m1, bool swiglu, const CUtensorMap& amap, const CUtensorMap& bmap, const Params& p,
-                       int smem, int grid, cudaStream_t stream) {
+                       int smem, dim3 grid, cudaStream_t stream) {
     if (e2m1)
         return swiglu ? launch<CG, true, true>(amap, bmap, p, smem, grid, stream)
                       : launch<CG, true, false>(amap, bmap, p, smem, grid, stream);
@@ -1019,6 +1053,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     const int64_t m_tiles = (a.t + rows - 1) / rows, n_tiles = (a.n + outputs - 1) / outputs;
     if (m_tiles * n_tiles >= (int64_t(1) << 27)) return cudaErrorInvalidValue;
     p.m_tiles = static_cast<int>(m_tiles);
+    p.n_tiles = static_cast<int>(n_tiles);
     p.tiles = static_cast<int>(m_tiles * n_tiles);
     p.rows_a = a.t < kRows ? static_cast<int>((a.t + 7) / 8 * 8) : kRows;
     p.rows_b = a.swiglu || c.cg == 2 ? c.width / 2 : c.width;
@@ -1030,7 +1065,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
                    : encode_spread_map(&bmap, a.wq, w_rows, a.k, p.rows_b);
     if (e != cudaSuccess) return e;
     const int cluster = c.cg * c.split, most = device->clusters[c.cg];
-    const int grid = cluster * (c.split > 1 || p.tiles < most ? p.tiles : most);
+    const dim3 grid(cluster, c.split > 1 || p.tiles < most ? p.tiles : most);
     return c.cg == 1 ? launch_any<1>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream)
                      : launch_any<2>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream);
 }
