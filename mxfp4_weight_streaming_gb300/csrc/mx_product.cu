@@ -64,6 +64,10 @@ constexpr int kAhead = 2;                  // groups that a warp loads ahead
 constexpr int kTmemCols = 512;             // all of them, so the allocation begins at column 0
 constexpr int kTurnRow = 80;               // 32 outputs of a token in shared memory, and a gap (banks)
 constexpr int kTurn = 32 * kTurnRow;       // a warp's
+// Shared memory that is asked for at least. Every kernel here that takes TMEM has
+// more than 64 KB, so none shares an SM with this one. CTAs of clusters that held
+// the columns of two SMs crosswise, each waiting for its other half, would never end.
+constexpr int kLeastShared = 192 * 1024;
 constexpr int kImage = 512;                // scales of 128 rows and 128 values
 
 // Columns for two accumulators (of 256 each they share some); the rest holds
@@ -751,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (bars.abort_flag() - raw));
     const WaitCtx wc{p.status, abort_flag};
     const Plan plan(p.width, CG, p.rows_a);
-    pdl_launch_dependents();
-    // What takes long is begun first: TMEM by the issuing warp, barriers by the copying one.
+    // What takes long is begun first: TMEM by the issuing warp, barriers by the copying one. The next kernel of the stream
+    // is let in after this one has its TMEM: the other way round it could take the columns and then wait for this kernel.
     if (warp == kMmaWarp) {
         if constexpr (CG == 1) {
             tc::tmem_alloc(bars.tmem_base(), kTmemCols);
@@ -761,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_alloc_pair(bars.tmem_base(), kTmemCols);
             tc::tmem_relinquish_pair();
         }
+        pdl_launch_dependents();
     }
     const bool alone = CG == 1 && p.split == 1;
     if (warp == kCopyWarp) {
@@ -968,6 +973,7 @@ bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
     while (c.ring < kMaxStages && plan.bytes(c.ring + 1, slots_for(c.ring + 1), turn) <= max_smem) ++c.ring;
     c.slots = slots_for(c.ring);
     c.smem = plan.bytes(c.ring, c.slots, turn);
+    if (c.smem < kLeastShared) c.smem = kLeastShared;
     return c.ring > 1;
 }
 
