@@ -560,7 +560,7 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
  * y[i][j] = bf16( sum_k x[i][k] * w[j][k] ) for any number of tokens.
  *   xq, xs  device MX codes (16-byte aligned) and scales (4-byte aligned) of x
  *           [t, k]; format: theirs
- *   k       a multiple of 128
+ *   k       a multiple of 128, at most 2^24
  *   wq, ws  device uint8 [n, k/2], [n, k/32], MXFP4 weights as for
  *           mxfp4_linear, wq 16-byte aligned (with E4M3 activations 32), ws 4;
  *           a scale byte of 255 is NaN

@@ -15,6 +15,7 @@ int launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUD
 bool known(int format) { return format == MXFP4_MX_E4M3 || format == MXFP4_MX_E2M1; }
 
 constexpr int64_t kMost = int64_t(1) << 31;  // coordinates of a copy are ints
+constexpr int64_t kMostK = int64_t(1) << 24; // a tile's sums over k stay far below the limit of a wait
 constexpr int64_t kMostStride = int64_t(1) << 31;
 
 // Memory of an operand. Outputs may not lie in the inputs: rows are read and
@@ -45,7 +46,7 @@ int product(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k,
     if (!xq || !xs || !wq || !ws || !y || (swiglu && !ys) || t <= 0 || k <= 0 || n <= 0 || !known(format) ||
         !known(out_format))
         return MXFP4_ERR_INVALID_ARG;
-    if (k % 128 || k >= kMost || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
+    if (k % 128 || k > kMostK || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
         return MXFP4_ERR_SHAPE;
     if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(wq, format == MXFP4_MX_E4M3 ? 32 : 16) ||
         !aligned(y, swiglu ? 16 : 2))

@@ -20,8 +20,8 @@
 // written once and read once at 128 bytes a cycle: 512 cycles for a pair's 256-wide
 // tile, 768 for a lone CTA's. Measured: 4,096 tokens x 7,168 x 2 x 18,432 gated 590
 // to 630 us (3.4 to 3.7 PFLOP/s, under the power cap), 4,096 x 18,432 x 7,168 in
-// E2M1 148 us (7.3), 512 x 7,168 x 9,216 26 us, 61 x 7,168 x 129,280 90 us (5.6
-// TB/s), 16 x 7,168 x 7,168 13 us, of which 8 are the call's beginning and end.
+// E2M1 147 us (7.4), 512 x 7,168 x 9,216 25.5 us, 61 x 7,168 x 129,280 90 us (5.6
+// TB/s), 16 x 7,168 x 7,168 12 to 13 us, of which 8 are the call's beginning and end.
 //
 // One CTA per SM walks over tiles, warp-specialised:
 //   0-7    epilogue: warp w reads the lanes (tokens) 32 (w % 4) .. of the
@@ -805,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cluster_sync_all();
         tc::fence_after_sync();
     };
+    // Every role waits for the previous kernel of the stream before its first bounded wait: that one may take long.
     bool summed = true;
     if (warp < kEpilogueWarps) {
         ready();
@@ -825,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         ready();
+        pdl_wait_previous();
         if (u.rank == 0 && !issue_products<CG, E2M1>(p, plan, u, base, bars, wc)) {
             // Products issued so far may still read shared memory and write TMEM: waited for, bounded.
             if (lane == 0) {
@@ -849,6 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scales.begin();
                 asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             }
+            if (set != 0) pdl_wait_previous();
             scales.run(wc);
         } else {
             ready();

@@ -53,7 +53,7 @@ def test_norm_refusals(change, status):
 @pytest.mark.parametrize("change,status", [
     (dict(xq=None), 1), (dict(xs=None), 1), (dict(wq=None), 1), (dict(ws=None), 1), (dict(y=None), 1), (dict(t=0), 1),
     (dict(k=0), 1), (dict(n=0), 1), (dict(format=2), 1), (dict(k=192), 2), (dict(k=32), 2), (dict(t=1 << 31), 2),
-    (dict(n=1 << 31), 2), (dict(k=1 << 31), 2), (dict(xq=A + 8), 3), (dict(xs=B + 2), 3), (dict(ws=D + 1), 3),
+    (dict(n=1 << 31), 2), (dict(k=1 << 31), 2), (dict(k=(1 << 24) + 128), 2), (dict(xq=A + 8), 3), (dict(xs=B + 2), 3), (dict(ws=D + 1), 3),
     (dict(wq=C + 16), 3), (dict(wq=C + 8, format=1), 3), (dict(y=E + 1), 3),
     (dict(y=A), 1), (dict(y=B + 4 * 8 - 2), 1), (dict(y=C - 2), 1), (dict(y=D), 1)])
 def test_linear_refusals(change, status):

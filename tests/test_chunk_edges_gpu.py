@@ -169,6 +169,20 @@ def test_weights_past_2_31():
         check(y[:, rows], ref, ref.abs() * 2.0 ** -8 + sum_bound(k, mag), f"rows {rows}")
 
 
+@pytest.mark.parametrize("form", ["e4m3", "e2m1"])
+def test_the_longest_k(form):
+    """k of 2^24, all but a few values 0: their sums are exact in fp32, so only the rounding to bf16 is left."""
+    mx, g = lib(), gen(19)
+    k = 1 << 24
+    x, w = torch.zeros(3, k, dtype=BF16, device="cuda"), random_codes(g, 5, k, "e2m1", spread=1)
+    at = torch.tensor([0, 5, 4097, k // 2 + 3, k - 129, k - 1], device="cuda")
+    x[:, at] = torch.tensor([[1.0, 2, 4, 1, 2, 1], [0, 0, 0, 0, 0, 1], [1, 0, 0, -4, 0, 0]], device="cuda").to(BF16)
+    y = mx.linear_mx(*mx.quantize_mx(x, form), *w)
+    assert mx.last_device_status() == mx.MXFP4_OK
+    ref = x[:, at].double() @ values(*w)[:, at].T
+    assert torch.equal(y, ref.to(BF16))
+
+
 def test_quantize_past_2_31():
     mx, g = lib(), gen(16)
     x = torch.empty(300000, 8192, dtype=BF16, device="cuda")
