@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(256, 8) mx_quantize_kernel(QuantizeParams p) {
             *reinterpret_cast<uint4*>(p.xq + e) = make_uint4(w[0], w[1], w[2], w[3]);
         if ((i & 1) == 0) p.xs[e / 32] = static_cast<uint8_t>(s);
     }
+    __threadfence();  // what a next kernel that begins when the last block ends may read at once
 }
 
 }  // namespace
