@@ -576,6 +576,32 @@ int mxfp4_linear_mx(const void* xq, const uint8_t* xs, int format, int64_t t, in
                     const uint8_t* ws, int64_t n, void* y, void* stream);
 
 /*
+ * How mxfp4_linear_mx (swiglu != 0: mxfp4_swiglu_mx, n = inter) cuts a product:
+ * what sets its speed, to be checked without a GPU (host only, no CUDA call).
+ *   t, k, n, format  as there (same checks of the sizes)
+ *   aligned_rows     whether rows of y begin at multiples of 16 bytes
+ *   max_smem         opt-in shared memory per block in bytes (232448 on GB300)
+ *   clusters         int32 [9]: of 1 .. 8 CTAs, one to an SM, so many clusters are
+ *                    resident at once (entry 0 unused); NULL: as on GB300
+ *   out              host struct, written on MXFP4_OK
+ */
+typedef struct {
+    int32_t pair;        /* 1: a pair of CTAs takes 256 tokens, 0: one takes 128 */
+    int32_t width;       /* weight rows of a tile (gate and up rows together) */
+    int32_t split;       /* CTAs or pairs of a cluster that share a tile's k */
+    int32_t ctas;        /* CTAs launched */
+    int32_t ring_slots;  /* stages in shared memory: 128 bytes of codes of every row */
+    int32_t stage_bytes;
+    int32_t token_rows;  /* rows of tokens in a stage */
+    int32_t scale_slots; /* groups of scales (512 values of k) in shared memory */
+    int32_t scale_bytes; /* of a group */
+    int32_t inbox_bytes; /* split > 1: of the others' sums, taken into the ring */
+    int32_t smem_bytes;  /* dynamic shared memory per CTA */
+} mxfp4_mx_plan_t;
+int mxfp4_linear_mx_plan(int64_t t, int64_t k, int64_t n, int format, int swiglu, int aligned_rows, int max_smem,
+                         const int32_t* clusters, mxfp4_mx_plan_t* out);
+
+/*
  * The gated half of an FFN, from codes to codes:
  *   h[i][j] = SiLU( sum_k x[i][k] w1[j][k] ) * sum_k x[i][k] w1[inter + j][k]
  * in fp32, and its MX codes (out_format), with no intermediate in memory.

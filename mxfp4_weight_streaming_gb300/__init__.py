@@ -18,7 +18,7 @@ cache_copy, cache_accept.
 
 Many tokens at once (activations as microscaled codes, and their products with
 MXFP4 weights) are in chunk.py and available from here: quantize_mx,
-residual_norm_mx, linear_mx, swiglu_mx.
+residual_norm_mx, linear_mx, swiglu_mx, linear_mx_plan (host only).
 """
 from __future__ import annotations
 
@@ -40,7 +40,7 @@ EXPORTED = ["mxfp4_strerror", "mxfp4_quantize", "mxfp4_linear", "mxfp4_linear_pl
             "mxfp4_moe", "mxfp4_last_device_status", "mxfp4_residual_norm", "mxfp4_rope_append",
             "mxfp4_attention_workspace_size", "mxfp4_attention", "mxfp4_attention_at", "mxfp4_cache_workspace_size",
             "mxfp4_cache_update", "mxfp4_cache_copy", "mxfp4_cache_accept", "mxfp4_quantize_mx",
-            "mxfp4_residual_norm_mx", "mxfp4_linear_mx", "mxfp4_swiglu_mx"]
+            "mxfp4_residual_norm_mx", "mxfp4_linear_mx", "mxfp4_linear_mx_plan", "mxfp4_swiglu_mx"]
 
 _lib = None
 
@@ -117,6 +117,8 @@ def load() -> ctypes.CDLL:
     L.mxfp4_residual_norm_mx.argtypes = [P, P, I64, I64, P, P, P, I64, F, P, P, F, F, I, I, P, P, P, P]
     L.mxfp4_linear_mx.restype = I
     L.mxfp4_linear_mx.argtypes = [P, P, I, I64, I64, P, P, I64, P, P]
+    L.mxfp4_linear_mx_plan.restype = I
+    L.mxfp4_linear_mx_plan.argtypes = [I64, I64, I64, I, I, I, I, P, P]
     L.mxfp4_swiglu_mx.restype = I
     L.mxfp4_swiglu_mx.argtypes = [P, P, I, I64, I64, P, P, I64, I, P, P, P]
     _lib = L
@@ -274,7 +276,7 @@ _STEP = ("KVBatch", "KVCache", "attention", "attention_workspace", "cache_accept
          "cache_workspace", "residual_norm", "rope_append", "rope_frequencies")
 
 
-_CHUNK = ("linear_mx", "quantize_mx", "residual_norm_mx", "swiglu_mx")
+_CHUNK = ("linear_mx", "linear_mx_plan", "quantize_mx", "residual_norm_mx", "swiglu_mx")
 
 
 def __getattr__(name):

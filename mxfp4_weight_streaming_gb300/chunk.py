@@ -10,6 +10,8 @@ the results it makes are that stream's memory.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import step
@@ -138,6 +140,25 @@ def linear_mx(xq, xs, wq, ws, out=None, stream=None):
     if rc:
         _fail(rc, "mxfp4_linear_mx")
     return y
+
+
+class MxPlan(ctypes.Structure):
+    """mxfp4_mx_plan_t: how linear_mx and swiglu_mx cut a product."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("pair", "width", "split", "ctas", "ring_slots", "stage_bytes",
+                                                     "token_rows", "scale_slots", "scale_bytes", "inbox_bytes", "smem_bytes")]
+
+
+def linear_mx_plan(t, k, n, format="e4m3", swiglu=False, aligned_rows=True, max_smem=232448, clusters=None):
+    """The plan for these sizes (swiglu: of swiglu_mx, n = inter) as a dict.
+    clusters: how many clusters of 1 .. 8 CTAs are resident at once (9 numbers,
+    the first unused; None: GB300's). Host only; raises Mxfp4Error when no plan fits."""
+    plan = MxPlan()
+    room = None if clusters is None else (ctypes.c_int32 * 9)(*clusters)
+    rc = _lib().mxfp4_linear_mx_plan(t, k, n, _format(format), bool(swiglu), bool(aligned_rows), max_smem, room,
+                                     ctypes.addressof(plan))
+    if rc:
+        _fail(rc, "mxfp4_linear_mx_plan")
+    return {name: getattr(plan, name) for name, _ in MxPlan._fields_}
 
 
 def swiglu_mx(xq, xs, w1q, w1s, format="e4m3", out=None, stream=None):

@@ -41,13 +41,19 @@ bool any_meet(std::initializer_list<Range> outputs, std::initializer_list<Range>
 
 int64_t code_bytes(int64_t values, int format) { return format == MXFP4_MX_E2M1 ? values / 2 : values; }
 
+// Of the sizes of a product.
+int product_shape(int64_t t, int64_t k, int64_t n, bool swiglu) {
+    if (k % 128 || k > kMostK || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
+        return MXFP4_ERR_SHAPE;
+    return MXFP4_OK;
+}
+
 int product(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq, const uint8_t* ws,
             int64_t n, bool swiglu, int out_format, void* y, uint8_t* ys, void* stream) {
     if (!xq || !xs || !wq || !ws || !y || (swiglu && !ys) || t <= 0 || k <= 0 || n <= 0 || !known(format) ||
         !known(out_format))
         return MXFP4_ERR_INVALID_ARG;
-    if (k % 128 || k > kMostK || t >= kMost - 256 || n >= (swiglu ? kMost / 2 : kMost) - 256 || (swiglu && n % 32))
-        return MXFP4_ERR_SHAPE;
+    if (int rc = product_shape(t, k, n, swiglu)) return rc;
     if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(wq, format == MXFP4_MX_E4M3 ? 32 : 16) ||
         !aligned(y, swiglu ? 16 : 2))
         return MXFP4_ERR_ALIGN;
@@ -145,6 +151,20 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
 int mxfp4_linear_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq,
                     const uint8_t* ws, int64_t n, void* y, void* stream) {
     return product(xq, xs, format, t, k, wq, ws, n, false, MXFP4_MX_E4M3, y, nullptr, stream);
+}
+
+int mxfp4_linear_mx_plan(int64_t t, int64_t k, int64_t n, int format, int swiglu, int aligned_rows, int max_smem,
+                         const int32_t* clusters, mxfp4_mx_plan_t* out) {
+    // Of 2 to 8 CTAs with most of an SM's shared memory each, as a GB300 holds them at once.
+    static const int32_t kGb300[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    if (t <= 0 || k <= 0 || n <= 0 || !known(format) || max_smem <= 0 || !out) return MXFP4_ERR_INVALID_ARG;
+    if (!clusters) clusters = kGb300;
+    for (int c = 1; c <= 8; ++c)
+        if (clusters[c] < (c == 1 ? 1 : 0)) return MXFP4_ERR_INVALID_ARG;
+    if (int rc = product_shape(t, k, n, swiglu != 0)) return rc;
+    return mxfp4::plan_mx_product(t, k, n, format == MXFP4_MX_E2M1, swiglu != 0, aligned_rows != 0, max_smem, clusters, out)
+               ? MXFP4_OK
+               : MXFP4_ERR_SHAPE;
 }
 
 int mxfp4_swiglu_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* w1q,

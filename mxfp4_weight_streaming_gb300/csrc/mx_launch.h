@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "mxfp4.h"
+
 namespace mxfp4 {
 
 struct MxQuantizeArgs {
@@ -33,6 +35,10 @@ struct MxProductArgs {
     unsigned* status;
 };
 cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem, cudaStream_t stream);
+
+// How the launch would cut a product, without a device: clusters[c] (1 to 8) of c CTAs, one to an SM, are resident at once.
+bool plan_mx_product(int64_t t, int64_t k, int64_t n, bool e2m1, bool swiglu, bool aligned, int max_smem,
+                     const int32_t* clusters, mxfp4_mx_plan_t* out);
 
 // Tensor maps (capi.cu). Codes as bytes [rows, row_bytes] in boxes of 128 bytes x box_rows, 128-byte swizzle.
 cudaError_t encode_code_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t row_bytes, int box_rows);

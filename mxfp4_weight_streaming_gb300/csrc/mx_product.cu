@@ -919,7 +919,7 @@ cudaError_t launch_any(bool e2m1, bool swiglu, const CUtensorMap& amap, const CU
 // What the choice of a tile needs to know of a device.
 struct Device {
     bool ready;
-    int sms, max_smem;
+    int max_smem;
     int clusters[9];  // of so many CTAs, one to an SM, that are resident at once
 };
 
@@ -937,7 +937,6 @@ cudaError_t device_of(const Device** out, int num_sms, int max_smem) {
                          configure<1, true, true>, configure<2, false, false>, configure<2, false, true>,
                          configure<2, true, false>, configure<2, true, true>})
             if ((e = set(max_smem))) return e;
-        d.sms = num_sms;
         d.max_smem = max_smem;
         d.clusters[1] = num_sms;
         for (int c = 2; c <= 8; ++c) {
@@ -962,10 +961,11 @@ cudaError_t device_of(const Device** out, int num_sms, int max_smem) {
 // A tile's shape and the CTAs that share its k.
 struct Choice {
     int cg, width, split, ring, slots, smem;
+    int inbox;  // bytes of the other parts' sums that a CTA takes into its ring
     float us;
 };
 
-// Stages in the ring, and slots for the scales of as many and two groups more; false if not even two fit.
+// Stages in the ring, and slots for the scales of as many and two groups more; false if not even two stages fit.
 bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
     const Plan plan(c.width, c.cg, rows_a);
     auto slots_for = [&](int ring) {
@@ -977,7 +977,7 @@ bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
     c.slots = slots_for(c.ring);
     c.smem = plan.bytes(c.ring, c.slots, turn);
     if (c.smem < kLeastShared) c.smem = kLeastShared;
-    return c.ring > 1;
+    return c.ring > 1 && c.smem <= max_smem;
 }
 
 // The tile with the least time by a model of what was measured on GB300 (in
@@ -1002,15 +1002,15 @@ Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn
             const int64_t tiles = ((t + kRows * cg - 1) / (kRows * cg)) * ((n + outputs - 1) / outputs);
             for (int split = 1; split * cg <= 8 && split <= groups; ++split) {
                 if (split > 1 && tiles > d.clusters[cg * split]) break;
-                Choice c{cg, width, split, 0, 0, 0, 0.f};
+                Choice c{cg, width, split, 0, 0, 0, 0, 0.f};
                 const int64_t waves = (tiles + d.clusters[cg] - 1) / d.clusters[cg];
                 const int longest = (groups + split - 1) / split * (kGroupWords / (e2m1 ? 2 : 1));
                 c.us = (split > 1 ? 1 : waves) * stage * (longest < stages ? longest : stages) + (cg == 1 ? 4.5f : 5.5f);
                 if (split > 1) c.us += 1.7f + rows_a * width * 4.f * (split - 1) / split / 20e3f;
                 if (c.us >= best.us || !fit(c, rows_a, e2m1, turn, d.max_smem)) continue;
                 // The sums of the others have to fit the ring (chunks of 32 columns, of both halves where swiglu).
-                const int inbox = (outputs / 32 + split - 1) / split * (split - 1) * kRows * 128 * (swiglu ? 2 : 1);
-                if (inbox > c.ring * Plan(width, cg, rows_a).stage) continue;
+                c.inbox = (outputs / 32 + split - 1) / split * (split - 1) * kRows * 128 * (swiglu ? 2 : 1);
+                if (c.inbox > c.ring * Plan(width, cg, rows_a).stage) continue;
                 best = c;
             }
         }
@@ -1020,6 +1020,33 @@ Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn
 
 }  // namespace
 }  // namespace mxp
+
+// How a product would be cut (host only).
+bool plan_mx_product(int64_t t, int64_t k, int64_t n, bool e2m1, bool swiglu, bool aligned, int max_smem,
+                     const int32_t* clusters, mxfp4_mx_plan_t* out) {
+    using namespace mxp;
+    Device d{};
+    d.max_smem = max_smem;
+    for (int c = 1; c <= 8; ++c) d.clusters[c] = clusters[c];
+    const Choice c = choose(t, n, k, e2m1, swiglu, !swiglu && !aligned, d);
+    if (!c.cg) return false;
+    const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows, outputs = swiglu ? c.width / 2 : c.width;
+    const Plan plan(c.width, c.cg, rows_a);
+    const int64_t tiles = ((t + kRows * c.cg - 1) / (kRows * c.cg)) * ((n + outputs - 1) / outputs);
+    *out = mxfp4_mx_plan_t{};
+    out->pair = c.cg == 2;
+    out->width = c.width;
+    out->split = c.split;
+    out->ctas = static_cast<int32_t>(c.cg * c.split * (c.split > 1 || tiles < clusters[c.cg] ? tiles : clusters[c.cg]));
+    out->ring_slots = c.ring;
+    out->stage_bytes = plan.stage;
+    out->token_rows = rows_a;
+    out->scale_slots = c.slots;
+    out->scale_bytes = plan.group;
+    out->inbox_bytes = c.inbox;
+    out->smem_bytes = c.smem;
+    return true;
+}
 
 cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem, cudaStream_t stream) {
     using namespace mxp;
