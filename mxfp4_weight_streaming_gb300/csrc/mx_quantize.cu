@@ -6,8 +6,8 @@
 // one thread wait while it computes, so an SM holds as many threads as it can
 // (32 registers each; with four rows' loads ahead in a thread and half as many
 // threads, 2,048 gated rows of 18,432 took 47 us). Bound by HBM: 16,384 rows of
-// 7,168 take 54.5 us, 96 % of the copy rate; gated ones by their instructions too
-// (issued in three cycles of four): 2,048 of 18,432 33 us, 84 %.
+// 7,168 take 55 us, 95 % of the copy rate; gated ones by their instructions too
+// (issued in three cycles of four): 2,048 of 18,432 34 us, 82 %.
 //
 // The next kernel of the stream is not let in early: it may take these codes
 // as weights, and the library's products read weights before they wait for the
