@@ -18,7 +18,8 @@ def guarded_codes(t, k, form):
 
 
 # ---------------------------------------------------------- quantisation
-@pytest.mark.parametrize("t,k", [(1, 32), (3, 64), (1, 7168), (5, 96), (2, 16384 + 32), (1000, 160), (70, 4096)])
+@pytest.mark.parametrize("t,k", [(1, 32), (3, 64), (1, 7168), (5, 96), (2, 16384 + 32), (1000, 160), (70, 4096),
+                                 (70001, 32), (5003, 96), (999, 2048), (300, 2080)])
 @pytest.mark.parametrize("form", FORMATS)
 def test_quantize(t, k, form):
     """Elements and scales bit by bit: x is bf16, its quotient by a power of two exact."""
@@ -89,7 +90,7 @@ def silu64(a):
     return a * torch.sigmoid(a)
 
 
-@pytest.mark.parametrize("t,k", [(1, 32), (3, 2048), (129, 96), (33, 18432)])
+@pytest.mark.parametrize("t,k", [(1, 32), (3, 2048), (129, 96), (33, 18432), (4001, 64)])
 @pytest.mark.parametrize("form", FORMATS)
 def test_quantize_swiglu(t, k, form):
     mx = lib()
