@@ -566,11 +566,9 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
  *           a scale byte of 255 is NaN
  *   y       device bf16 [t, n], 2-byte aligned (output; 16-byte aligned with
  *           n % 8 == 0 takes the wide stores)
- * Products of codes are exact, sums fp32 in the tensor cores' order. Weights are
- * read before the previous kernel of the stream has ended: they may come from
- * mxfp4_quantize, mxfp4_quantize_mx or anything outside the library, but not from
- * the mxfp4_residual_norm_mx or mxfp4_swiglu_mx call right before, whose codes are
- * activations.
+ * Products of codes are exact, sums fp32 in the tensor cores' order. Activations
+ * and weights may come from any earlier work of the stream, the call right before
+ * included: nothing is read before it has ended.
  */
 int mxfp4_linear_mx(const void* xq, const uint8_t* xs, int format, int64_t t, int64_t k, const uint8_t* wq,
                     const uint8_t* ws, int64_t n, void* y, void* stream);

@@ -243,15 +243,15 @@ struct Copier {
     }
     // Test-only builds: the first cluster's first CTA never gets its first stage.
     __device__ __forceinline__ bool withheld(int j) const { return u.first == 0 && withhold_stage(static_cast<uint32_t>(j)); }
-    // The weights of the ring's first round. They do not wait for the previous kernel of the stream.
-    __device__ __forceinline__ void begin() const {
-        for (int j = 0; j < first; ++j)
-            if (!withheld(j)) weights(j, u.stage0 + j);
-    }
+    // The previous kernel of the stream may still write tokens and weights: nothing is read before it has ended. (Weights
+    // fetched ahead into L2, which is safe too, cost more than they brought: 16 tokens 14.5 us against 12.3 to 13.2.)
     __device__ __forceinline__ void run(const WaitCtx& wc) {
-        pdl_wait_previous();  // it may still write the tokens
-        for (int j = 0; j < first; ++j)
-            if (!withheld(j)) tokens(j, u.stage0 + j);
+        pdl_wait_previous();
+        for (int j = 0; j < first; ++j) {
+            if (withheld(j)) continue;
+            weights(j, u.stage0 + j);
+            tokens(j, u.stage0 + j);
+        }
         Ring r;
         int issued = 0;
         bool ok = true;
@@ -380,7 +380,7 @@ struct Scales {
         skip();
         if (tile < p.tiles) skip();
     }
-    // The first groups: of weights at once, of tokens when the previous kernel, which may write them, has ended.
+    // The first groups, when the previous kernel of the stream, which may write them, has ended.
     __device__ __forceinline__ void begin() {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) load(v[d]);
@@ -755,8 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + (bars.abort_flag() - raw));
     const WaitCtx wc{p.status, abort_flag};
     const Plan plan(p.width, CG, p.rows_a);
-    // What takes long is begun first: TMEM by the issuing warp, barriers by the copying one. The next kernel of the stream
-    // is let in after this one has its TMEM: the other way round it could take the columns and then wait for this kernel.
+    // What takes long is begun first: TMEM by the issuing warp, barriers by the copying one.
     if (warp == kMmaWarp) {
         if constexpr (CG == 1) {
             tc::tmem_alloc(bars.tmem_base(), kTmemCols);
@@ -765,7 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_alloc_pair(bars.tmem_base(), kTmemCols);
             tc::tmem_relinquish_pair();
         }
-        pdl_launch_dependents();
     }
     const bool alone = CG == 1 && p.split == 1;
     if (warp == kCopyWarp) {
@@ -776,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bars.init(lane, static_cast<uint32_t>(CG * plan.sets), CG * kEpilogueWarps);
         __syncwarp();
-        // It goes on to the first copies while the others wait for barriers and TMEM.
+        // It goes on to the first copies while the others wait for TMEM.
         if (alone)
             asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
         else
@@ -817,16 +815,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             summed = wait_all(bars.acc_full(0), 0, wc);  // a cluster has one tile
     } else if (warp == kCopyWarp) {
         Copier<CG, E2M1, SWIGLU> copier(p, plan, u, &amap, &bmap, base, bars);
-        if (lane == 0 && u.rank == 0) copier.begin();  // on barriers of its own
-        __syncwarp();
         if (!alone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (lane == 0) {
-            if (u.rank != 0) copier.begin();
-            copier.run(wc);
-        }
+        if (lane == 0) copier.run(wc);
     } else if (warp == kMmaWarp) {
         ready();
+        // The next kernel of the stream is let in once this one has its TMEM (the other way round it could take the columns
+        // and then wait for this kernel) and the previous one has ended: other calls of the library read weights before they
+        // wait, and what they wait for is only the kernel right ahead of them.
         pdl_wait_previous();
+        pdl_launch_dependents();
         if (u.rank == 0 && !issue_products<CG, E2M1>(p, plan, u, base, bars, wc)) {
             // Products issued so far may still read shared memory and write TMEM: waited for, bounded.
             if (lane == 0) {
@@ -842,16 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             Scales<CG, SWIGLU> scales(p, plan, u, set, (warp - kScaleWarp) / 3, lane, base, bars);
             if (alone) {
                 ready();
-                if (set == 0) pdl_wait_previous();
+                pdl_wait_previous();
                 scales.begin();
             } else {
                 // The cluster's barrier would wait for loads under way.
                 asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-                if (set == 0) pdl_wait_previous();
+                pdl_wait_previous();
                 scales.begin();
                 asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             }
-            if (set != 0) pdl_wait_previous();
             scales.run(wc);
         } else {
             ready();
