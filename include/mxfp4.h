@@ -34,6 +34,16 @@
  *     caller's own buffers. Exception: calls of mxfp4_moe_noalloc that
  *     overlap on the GPU (unordered streams, or threads) race on its
  *     shared scratch array.
+ *   - mxfp4_linear, mxfp4_ffn and mxfp4_moe (and their forms) read weights and
+ *     their scales before earlier kernels of the stream have ended. What
+ *     mxfp4_quantize and mxfp4_quantize_mx write is complete by then: they let
+ *     no other kernel begin before their stores are performed. So is what a
+ *     copy brings. Weights that any other kernel writes (one of another
+ *     library; mxfp4_residual_norm_mx and mxfp4_swiglu_mx, whose E2M1 codes are
+ *     activations) have to be complete before such a call, however many calls
+ *     lie between: by a wait on the host, by an event of another stream, or by
+ *     a copy or memset in this one. mxfp4_linear_mx and mxfp4_swiglu_mx read
+ *     nothing ahead and take weights from anything.
  *   - The first call on a device looks up per-device addresses (the status
  *     word, the mxfp4_moe_noalloc scratch) and keeps them for the life of
  *     the process. After cudaDeviceReset, or anything else that replaces

@@ -194,6 +194,9 @@ def quantize(w, stream=None):
     return wq, ws
 
 
+# linear, moe and ffn read weights before earlier kernels of the stream have
+# ended: weights come from quantize, quantize_mx, copies, or kernels that were
+# waited for (include/mxfp4.h, conventions).
 def linear(x, wq, ws, out=None, stream=None):
     """bf16 x [t, k] @ dequant(wq, ws)^T -> bf16 y [t, n]."""
     import torch

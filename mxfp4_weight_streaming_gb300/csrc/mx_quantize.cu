@@ -10,8 +10,8 @@
 // (issued in three cycles of four): 2,048 of 18,432 34 us, 82 %.
 //
 // The next kernel of the stream is not let in early: it may take these codes
-// as weights, and the library's products read weights before they wait for the
-// kernel ahead of them.
+// as weights, and mxfp4_linear and others read weights before they wait for the
+// kernels ahead of them.
 #include <type_traits>
 
 #include "mx_common.cuh"

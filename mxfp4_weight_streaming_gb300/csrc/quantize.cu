@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const float* __restrict__
         reinterpret_cast<uint4*>(wq)[i] = make_uint4(out[0], out[1], out[2], out[3]);
         ws[i] = static_cast<uint8_t>(s);
     }
+    __threadfence();  // what a next kernel that begins when the last block ends may read at once
 }
 
 cudaError_t launch_quantize(const float* w, int64_t n, int64_t k, uint8_t* wq, uint8_t* ws, cudaStream_t stream,

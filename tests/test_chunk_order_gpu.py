@@ -61,6 +61,7 @@ def unrelated(kind):
         return lambda: mx.linear_mx(*a, *w)
     if kind == "linear":
         a, w = randn(g, 2, 512), random_codes(g, 64, 512, "e2m1")
+        torch.cuda.synchronize()
         return lambda: mx.linear(a, *w)
     return lambda: None
 
@@ -96,3 +97,21 @@ def test_products_of_many_tokens(maker, between, n, k):
         x = random_codes(g, t, k, form)
         same_as_apart(getattr(m, maker), steps, lambda: (mx.linear_mx(*x, m.q, m.s),))
         same_as_apart(getattr(m, maker), steps, lambda: mx.swiglu_mx(*x, m.q, m.s))
+
+
+@pytest.mark.parametrize("between", [(), ("linear_mx",), ("linear",), ("linear_mx", "linear")])
+@pytest.mark.parametrize("maker", ["quantize", "quantize_mx"])
+@pytest.mark.parametrize("n,k", [(64, 512), (640, 2048), (640, 1056)])
+def test_calls_that_read_weights_ahead(maker, between, n, k):
+    """mxfp4_linear's three kernels and the FFN's two read weights before they wait for the kernels ahead of them, which
+    both packers allow for."""
+    mx, g = lib(), gen(4)
+    m = Makers(n, k)
+    steps = [unrelated(b) for b in between]
+    for t in (3, 20):
+        x = randn(g, t, k)
+        same_as_apart(getattr(m, maker), steps, lambda: (mx.linear(x, m.q, m.s),))
+    w2 = mx.quantize(torch.randn(k, n // 2, generator=g, device="cuda"))
+    for t in (2, 7):
+        x = randn(g, t, k)
+        same_as_apart(getattr(m, maker), steps, lambda: (mx.ffn(x, m.q, m.s, *w2),))
