@@ -538,7 +538,8 @@ int mxfp4_cache_accept(const mxfp4_kv_cache_t* cache, const mxfp4_kv_batch_t* ba
  * are rounded to nearest, ties to even. A block that holds a NaN or an
  * infinity gets scale 255, NaN, and every output it takes part in is NaN.
  * (mxfp4_quantize's rule for weights is another: theirs may saturate.)
- * Outputs may not overlap inputs or each other (but r_out may be residual or x).
+ * Outputs may not overlap inputs or each other (but r_out may be residual or x,
+ * at the same address).
  */
 typedef enum {
     MXFP4_MX_E4M3 = 0, /* 8 bits: 4 significant ones, 8.25 bits a value in all */

@@ -122,8 +122,12 @@ int mxfp4_residual_norm_mx(const void* x, const void* residual, int64_t tokens, 
     const Range r{r_out, 2 * tokens * n}, codes{yq, code_bytes(tokens * n, format)}, scales{ys, tokens * n / 32};
     const int64_t gate_bytes = gate ? 2 * ((tokens - 1) * gate_stride + n) : 0;
     if (any_meet({codes, scales}, {r, {x, 2 * tokens * n}, {residual, 2 * tokens * n}, {gate, gate_bytes}, {weight, 2 * n},
-                                   {bias, 2 * n}, {post_weight, 2 * n}, {post_bias, 2 * n}}))
+                                   {bias, 2 * n}, {post_weight, 2 * n}, {post_bias, 2 * n}}) ||
+        any_meet({r}, {{gate, gate_bytes}, {weight, 2 * n}, {bias, 2 * n}, {post_weight, 2 * n}, {post_bias, 2 * n}}))
         return MXFP4_ERR_INVALID_ARG;
+    // r may be x or the residual as they lie: a row is read before it is written. Shifted, it would be another's row.
+    for (const void* p : {x, residual})
+        if (p != r_out && r.meets({p, 2 * tokens * n})) return MXFP4_ERR_INVALID_ARG;
     mxfp4::DeviceCaps caps;
     if (int rc = mxfp4::device_caps(&caps)) return rc;
     mxfp4::ResidualNormArgs a{};

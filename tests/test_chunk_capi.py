@@ -66,3 +66,13 @@ def test_linear_refusals(change, status):
     (dict(hq=E + 8), 3), (dict(hq=A), 1), (dict(hs=E), 1), (dict(hs=D + 2 * 96 * 8 - 1), 1)])
 def test_swiglu_refusals(change, status):
     assert call("mxfp4_swiglu_mx", SWIGLU, change) == status
+
+
+@pytest.mark.parametrize("change", [
+    dict(r_out=C), dict(r_out=C + 496), dict(bias=F, r_out=F), dict(post_weight=F + 2032, r_out=F),
+    dict(post_weight=A, post_bias=F, r_out=F), dict(gate=F, r_out=F), dict(gate=F, gate_stride=256, r_out=F),
+    dict(gate=F - 3 * 1024 - 496, gate_stride=512, r_out=F), dict(r_out=A + 512), dict(r_out=A - 16), dict(r_out=B + 512),
+    dict(r_out=B - 2032)])
+def test_norm_refuses_a_sum_over_its_inputs(change):
+    """r over a vector that every row reads, over the gates, or over x or the residual a few rows on."""
+    assert call("mxfp4_residual_norm_mx", NORM, change) == 1
