@@ -88,23 +88,57 @@ __device__ __forceinline__ void encode(const float* v, uint32_t s, uint32_t (&ou
     }
 }
 
-// z[i] = SiLU(z[i]) * up[i] = z / (1 + 2^(-z log2 e)) * up in fp32, two at a time.
-// The power may overflow to infinity: its reciprocal is the right 0.
-template <int N>
-__device__ __forceinline__ void swiglu(float* z, const float* up) {
+// SiLU(z) * up = z / (1 + 2^(-z log2 e)) * up in fp32, of two values.
+__device__ __forceinline__ float2 gated(float z0, float z1, float up0, float up1) {
     const uint64_t minus_log2e = f32x2_pack(-1.44269504f, -1.44269504f), one = f32x2_pack(1.f, 1.f);
+    const uint64_t a = f32x2_pack(z0, z1);
+    float2 e = f32x2_unpack(f32x2_mul(a, minus_log2e));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    float2 d = f32x2_unpack(f32x2_fma(f32x2_pack(e.x, e.y), one, one));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.y));
+    return f32x2_unpack(f32x2_mul(f32x2_mul(a, f32x2_pack(d.x, d.y)), f32x2_pack(up0, up1)));
+}
+
+// Below this gate the power comes near the end of fp32's range and its reciprocal is
+// lost, though up may be large enough for the product to count. There the 1 beside
+// the power does not, and the product is (z e^(z/2)) (up e^(z/2)), no part of which
+// leaves the range before the whole does.
+constexpr float kFarGate = -87.f;
+__device__ __forceinline__ float far_gated(float z, float up) {
+    float half;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(half) : "f"(z * 0.72134752f));
+    return (z * half) * (up * half);
+}
+
+__device__ __forceinline__ float gated_any(float z, float up) {
+    return z < kFarGate ? far_gated(z, up) : gated(z, z, up, up).x;
+}
+
+// z[i] = SiLU(z[i]) * up[i], of gates that are not below kFarGate.
+template <int N>
+__device__ __forceinline__ void swiglu_near(float* z, const float* up) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const uint64_t a = f32x2_pack(z[i], z[i + 1]);
-        float2 e = f32x2_unpack(f32x2_mul(a, minus_log2e));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-        float2 d = f32x2_unpack(f32x2_fma(f32x2_pack(e.x, e.y), one, one));
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.x));
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.y));
-        const float2 h = f32x2_unpack(f32x2_mul(f32x2_mul(a, f32x2_pack(d.x, d.y)), f32x2_pack(up[i], up[i + 1])));
+        const float2 h = gated(z[i], z[i + 1], up[i], up[i + 1]);
         z[i] = h.x;
         z[i + 1] = h.y;
+    }
+}
+
+// The same of any gates; each value comes out the same whatever stands beside it.
+template <int N>
+__device__ __forceinline__ void swiglu(float* z, const float* up) {
+    float low = fminf(z[0], z[1]);
+#pragma unroll
+    for (int i = 2; i < N; i += 2) asm("min.f32 %0, %0, %1, %2;" : "+f"(low) : "f"(z[i]), "f"(z[i + 1]));
+    if (!(low < kFarGate)) return swiglu_near<N>(z, up);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 h = gated(z[i], z[i + 1], up[i], up[i + 1]);
+        z[i] = z[i] < kFarGate ? far_gated(z[i], up[i]) : h.x;
+        z[i + 1] = z[i + 1] < kFarGate ? far_gated(z[i + 1], up[i + 1]) : h.y;
     }
 }
 

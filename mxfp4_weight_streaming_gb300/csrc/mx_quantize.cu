@@ -7,7 +7,8 @@
 // (32 registers each; with four rows' loads ahead in a thread and half as many
 // threads, 2,048 gated rows of 18,432 took 47 us). Bound by HBM: 16,384 rows of
 // 7,168 take 55 us, 95 % of the copy rate; gated ones by their instructions too
-// (issued in three cycles of four): 2,048 of 18,432 34 us, 82 %.
+// (issued in three cycles of four): 2,048 of 18,432 35 us, 80 % (34 without the
+// way for gates below -87).
 //
 // The next kernel of the stream is not let in early: it may take these codes
 // as weights, and mxfp4_linear and others read weights before they wait for the
@@ -50,6 +51,25 @@ __device__ __forceinline__ Half load_half(const __nv_bfloat16* p) {
     return h;
 }
 
+// Whether one of 16 gates is below kFarGate (or a NaN with its sign set). As unsigned
+// halfwords negative numbers are above the others, and the larger the lower.
+__device__ __forceinline__ bool far_gates(const Half& h) {
+    constexpr uint32_t kFar = 0xc2ae;  // bf16 of -87
+    static_assert(mx::kFarGate == -87.f, "its bits");
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&h);
+    uint32_t m = __vimax3_u16x2(w[0], w[1], w[2]);
+    m = __vimax3_u16x2(m, w[3], w[4]);
+    m = __vimax3_u16x2(m, w[5], w[6]);
+    m = __vmaxu2(m, w[7]);
+    return (m >> 16) > kFar || (m & 0xffffu) > kFar;
+}
+
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
+    uint16_t h;
+    asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+    return __uint_as_float(static_cast<uint32_t>(h) << 16);
+}
+
 // SHORT: rows of at most 2,048 values, several side by side in a block (1,000,000
 // rows of 32 take 16 us, with a block a row 497). Longer ones do without the
 // division: 2,048 gated rows of 18,432 34 us against 39.
@@ -76,7 +96,12 @@ __global__ void __launch_bounds__(256, 8) mx_quantize_kernel(QuantizeParams p) {
             float up[16];
             unpack8(b.v[0], *reinterpret_cast<float(*)[8]>(up));
             unpack8(b.v[1], *reinterpret_cast<float(*)[8]>(up + 8));
-            mx::swiglu<16>(z, up);
+            mx::swiglu_near<16>(z, up);
+            // All over again, from memory: kept, the gates and up values would not fit the 32 registers.
+            if (far_gates(a)) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = mx::gated_any(load_one(src + j), load_one(src + k + j));
+            }
         }
         uint32_t top = mx::largest<16>(z);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
