@@ -961,6 +961,9 @@ struct Choice {
     float us;
 };
 
+// Rows of tokens in a stage.
+int token_rows(int64_t t) { return t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows; }
+
 // Stages in the ring, and slots for the scales of as many and two groups more; false if not even two stages fit.
 bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
     const Plan plan(c.width, c.cg, rows_a);
@@ -988,7 +991,7 @@ bool fit(Choice& c, int rows_a, bool e2m1, bool turn, int max_smem) {
 Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn, const Device& d) {
     const int stages = static_cast<int>((k + (e2m1 ? 255 : 127)) / (e2m1 ? 256 : 128));
     const int groups = static_cast<int>((k / 128 + kGroupWords - 1) / kGroupWords);
-    const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows;
+    const int rows_a = token_rows(t);
     Choice best{};
     best.us = 1e30f;
     for (int cg = 1; cg <= (t > kRows && d.clusters[2] > 0 ? 2 : 1); ++cg) {
@@ -1014,6 +1017,30 @@ Choice choose(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn
     return best;
 }
 
+// A choice and what the launch makes of it.
+struct Cut {
+    Choice c;                  // c.cg == 0: none fits
+    int rows_a, rows_b;        // rows of a copied box
+    int64_t m_tiles, n_tiles;
+    int cluster, rows;         // of the grid: CTAs of a cluster, and clusters
+};
+
+Cut cut(int64_t t, int64_t n, int64_t k, bool e2m1, bool swiglu, bool turn, const Device& d) {
+    Cut r{};
+    const Choice c = r.c = choose(t, n, k, e2m1, swiglu, turn, d);
+    if (!c.cg) return r;
+    const int outputs = swiglu ? c.width / 2 : c.width, rows = kRows * c.cg;
+    r.rows_a = token_rows(t);
+    r.rows_b = swiglu || c.cg == 2 ? c.width / 2 : c.width;
+    r.m_tiles = (t + rows - 1) / rows;
+    r.n_tiles = (n + outputs - 1) / outputs;
+    const int64_t tiles = r.m_tiles * r.n_tiles;
+    if (tiles >= (int64_t(1) << 27)) return Cut{};
+    r.cluster = c.cg * c.split;
+    r.rows = static_cast<int>(c.split > 1 || tiles < d.clusters[c.cg] ? tiles : d.clusters[c.cg]);
+    return r;
+}
+
 }  // namespace
 }  // namespace mxp
 
@@ -1024,19 +1051,18 @@ bool plan_mx_product(int64_t t, int64_t k, int64_t n, bool e2m1, bool swiglu, bo
     Device d{};
     d.max_smem = max_smem;
     for (int c = 1; c <= 8; ++c) d.clusters[c] = clusters[c];
-    const Choice c = choose(t, n, k, e2m1, swiglu, !swiglu && !aligned, d);
+    const Cut r = cut(t, n, k, e2m1, swiglu, !swiglu && !aligned, d);
+    const Choice& c = r.c;
     if (!c.cg) return false;
-    const int rows_a = t < kRows ? static_cast<int>((t + 7) / 8 * 8) : kRows, outputs = swiglu ? c.width / 2 : c.width;
-    const Plan plan(c.width, c.cg, rows_a);
-    const int64_t tiles = ((t + kRows * c.cg - 1) / (kRows * c.cg)) * ((n + outputs - 1) / outputs);
+    const Plan plan(c.width, c.cg, r.rows_a);
     *out = mxfp4_mx_plan_t{};
     out->pair = c.cg == 2;
     out->width = c.width;
     out->split = c.split;
-    out->ctas = static_cast<int32_t>(c.cg * c.split * (c.split > 1 || tiles < clusters[c.cg] ? tiles : clusters[c.cg]));
+    out->ctas = r.cluster * r.rows;
     out->ring_slots = c.ring;
     out->stage_bytes = plan.stage;
-    out->token_rows = rows_a;
+    out->token_rows = r.rows_a;
     out->scale_slots = c.slots;
     out->scale_bytes = plan.group;
     out->inbox_bytes = c.inbox;
@@ -1053,7 +1079,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
         int64_t t, n, k;
         const Device* device;
         int kind;
-        Choice choice;
+        Cut cut;
     };
     thread_local Kept kept[16];
     const uintptr_t rows_at = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(2 * a.n);
@@ -1062,10 +1088,9 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     const int kind = (a.e2m1 ? 2 : 0) + (a.swiglu ? 1 : 0) + (turn ? 4 : 0);
     Kept& slot = kept[(a.t * 31 + a.n * 7 + a.k / 128 + kind) & 15];
     if (slot.device != device || slot.t != a.t || slot.n != a.n || slot.k != a.k || slot.kind != kind)
-        slot = Kept{a.t, a.n, a.k, device, kind, choose(a.t, a.n, a.k, a.e2m1, a.swiglu, turn, *device)};
-    const Choice& c = slot.choice;
+        slot = Kept{a.t, a.n, a.k, device, kind, cut(a.t, a.n, a.k, a.e2m1, a.swiglu, turn, *device)};
+    const Choice& c = slot.cut.c;
     if (!c.cg) return cudaErrorInvalidValue;
-    const int outputs = a.swiglu ? c.width / 2 : c.width, rows = kRows * c.cg;
     Params p{};
     p.xs = a.xs;
     p.ws = a.ws;
@@ -1082,13 +1107,11 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
     p.out_e2m1 = a.out_e2m1;
     p.align = align;
     p.stages = static_cast<int>((a.k + (a.e2m1 ? 255 : 127)) / (a.e2m1 ? 256 : 128));
-    const int64_t m_tiles = (a.t + rows - 1) / rows, n_tiles = (a.n + outputs - 1) / outputs;
-    if (m_tiles * n_tiles >= (int64_t(1) << 27)) return cudaErrorInvalidValue;
-    p.m_tiles = static_cast<int>(m_tiles);
-    p.n_tiles = static_cast<int>(n_tiles);
-    p.tiles = static_cast<int>(m_tiles * n_tiles);
-    p.rows_a = a.t < kRows ? static_cast<int>((a.t + 7) / 8 * 8) : kRows;
-    p.rows_b = a.swiglu || c.cg == 2 ? c.width / 2 : c.width;
+    p.m_tiles = static_cast<int>(slot.cut.m_tiles);
+    p.n_tiles = static_cast<int>(slot.cut.n_tiles);
+    p.tiles = p.m_tiles * p.n_tiles;
+    p.rows_a = slot.cut.rows_a;
+    p.rows_b = slot.cut.rows_b;
     const int64_t w_rows = a.swiglu ? 2 * a.n : a.n;
     CUtensorMap amap, bmap;
     cudaError_t e = encode_code_map(&amap, a.xq, a.t, a.e2m1 ? a.k / 2 : a.k, p.rows_a);
@@ -1096,8 +1119,7 @@ cudaError_t launch_mx_product(const MxProductArgs& a, int num_sms, int max_smem,
         e = a.e2m1 ? encode_code_map(&bmap, a.wq, w_rows, a.k / 2, p.rows_b)
                    : encode_spread_map(&bmap, a.wq, w_rows, a.k, p.rows_b);
     if (e != cudaSuccess) return e;
-    const int cluster = c.cg * c.split, most = device->clusters[c.cg];
-    const dim3 grid(cluster, c.split > 1 || p.tiles < most ? p.tiles : most);
+    const dim3 grid(slot.cut.cluster, slot.cut.rows);
     return c.cg == 1 ? launch_any<1>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream)
                      : launch_any<2>(a.e2m1, a.swiglu, amap, bmap, p, c.smem, grid, stream);
 }

@@ -98,3 +98,10 @@ def test_too_little_shared_memory():
             mx.linear_mx_plan(4096, 7168, 7168, max_smem=most)
     with pytest.raises(mx.Mxfp4Error):
         mx.linear_mx_plan(4, 256, 40, swiglu=True)  # inter
+
+
+def test_more_tiles_than_a_launch_counts():
+    """No plan for what a launch would refuse: 2^27 tiles and more."""
+    assert mx.linear_mx_plan(1 << 24, 128, 1 << 18)["ctas"] > 0
+    with pytest.raises(mx.Mxfp4Error):
+        mx.linear_mx_plan(1 << 30, 128, 1 << 30)
