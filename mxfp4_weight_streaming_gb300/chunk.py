@@ -7,6 +7,10 @@ MX codes of [t, k] activations are a pair of tensors: float8_e4m3fn [t, k] or
 uint8 [t, k / 2] (E2M1, two a byte), and uint8 scales [t, k / 32]. All tensors
 of a call lie on the current GPU. With stream= a call runs on that stream, and
 the results it makes are that stream's memory.
+
+linear_mx and swiglu_mx take weights from whatever ran before. linear, moe and
+ffn read theirs ahead: E2M1 codes of residual_norm_mx or swiglu_mx have to be
+waited for before they serve those as weights, quantize_mx's need not be.
 """
 from __future__ import annotations
 

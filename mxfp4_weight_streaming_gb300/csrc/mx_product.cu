@@ -18,10 +18,12 @@
 // What bounds a stage: its products (512 cycles at 128 x 256 per SM in E4M3, and no
 // less than 119 each however narrow), and shared memory, where every byte is
 // written once and read once at 128 bytes a cycle: 512 cycles for a pair's 256-wide
-// tile, 768 for a lone CTA's. Measured: 4,096 tokens x 7,168 x 2 x 18,432 gated 590
-// to 630 us (3.4 to 3.7 PFLOP/s, under the power cap), 4,096 x 18,432 x 7,168 in
-// E2M1 147 us (7.4), 512 x 7,168 x 9,216 25.5 us, 61 x 7,168 x 129,280 90 us (5.6
-// TB/s), 16 x 7,168 x 7,168 12 to 13 us, of which 8 are the call's beginning and end.
+// tile, 768 for a lone CTA's. Measured in CUDA graphs (and as calls from Python one
+// after another, warmer): 4,096 tokens x 7,168 x 2 x 18,432 gated 610 to 645 us (653;
+// 3.4 to 3.5 PFLOP/s, under the power cap), 4,096 x 18,432 x 7,168 in E2M1 150 us
+// (167; 7.2 and 6.5), 512 x 7,168 x 9,216 25.7 us (27), 61 x 7,168 x 129,280 92 to 94
+// us (100; 5.5 TB/s), 16 x 7,168 x 7,168 12 to 13 us (13), of which the products take
+// 4 and the rest is the call's beginning, the exchange of its sums and its end.
 //
 // One CTA per SM walks over tiles, warp-specialised:
 //   0-7    epilogue: warp w reads the lanes (tokens) 32 (w % 4) .. of the

@@ -6,9 +6,9 @@
 // one thread wait while it computes, so an SM holds as many threads as it can
 // (32 registers each; with four rows' loads ahead in a thread and half as many
 // threads, 2,048 gated rows of 18,432 took 47 us). Bound by HBM: 16,384 rows of
-// 7,168 take 55 us, 95 % of the copy rate; gated ones by their instructions too
-// (issued in three cycles of four): 2,048 of 18,432 35 us, 80 % (34 without the
-// way for gates below -87).
+// 7,168 take 55 us, 95 % of the copy rate; gated ones by waiting for their loads:
+// 2,048 of 18,432 35 us, 79 % (34 without the way for gates below -87, which
+// costs registers), 33 as E2M1.
 //
 // The next kernel of the stream is not let in early: it may take these codes
 // as weights, and mxfp4_linear and others read weights before they wait for the
@@ -72,7 +72,8 @@ __device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
 
 // SHORT: rows of at most 2,048 values, several side by side in a block (1,000,000
 // rows of 32 take 16 us, with a block a row 497). Longer ones do without the
-// division: 2,048 gated rows of 18,432 34 us against 39.
+// division: 2,048 gated rows of 18,432 34 us against 39 (both without the way for
+// gates below -87).
 template <bool SWIGLU, bool E2M1, bool WIDE, bool SHORT>
 __global__ void __launch_bounds__(256, 8) mx_quantize_kernel(QuantizeParams p) {
     // This thread's place in a row, and its row among those side by side. Halves are even, so that a block's two threads are

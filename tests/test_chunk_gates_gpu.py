@@ -138,3 +138,22 @@ def test_linear_not_finite(t, n, k, form):
     assert y[bad].isnan().all()
     assert torch.equal(y[~bad].view(torch.int16), want[~bad].view(torch.int16))
     assert U8 is wq.dtype
+
+
+@pytest.mark.parametrize("t,inter,k", [(4, 2048, 7168), (300, 2048, 2048), (1100, 4096, 512)])
+@pytest.mark.parametrize("form", FORMATS)
+def test_same_bits_every_time(form, t, inter, k):
+    """Norm, gated product and product, one after another, many times."""
+    mx, g = lib(), gen(8)
+    x, res, w = randn(g, t, k), randn(g, t, k), randn(g, k) * 0.1 + 1
+    w1 = mx.quantize(torch.randn(2 * inter, k, generator=g, device="cuda") * k ** -0.5)
+    w2 = mx.quantize(torch.randn(k, inter, generator=g, device="cuda") * inter ** -0.5)
+
+    def block():
+        q, s, r = mx.residual_norm_mx(x, res, w, format=form)
+        h = mx.swiglu_mx(q, s, *w1, format=form)
+        return [v.contiguous().view(U8) for v in (q, s, r, *h, mx.linear_mx(*h, *w2))]
+
+    first = block()
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(block(), first))

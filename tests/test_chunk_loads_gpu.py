@@ -3,9 +3,9 @@ only, by the rows' begin or by their stride, short and long rows, gated or not."
 import pytest
 import torch
 
-from chunk_cases import E4M3, elements, round_to, scale_exponents
+from chunk_cases import E4M3, elements, product, round_to, scale_exponents, sum_bound
 from gpu_cases import Guarded, lib
-from step_cases import gen, randn
+from step_cases import check, gen, randn
 
 pytestmark = pytest.mark.gpu
 BF16, U8 = torch.bfloat16, torch.uint8
@@ -46,4 +46,25 @@ def test_gated_rows(form, t, k, before, between):
     x = rows(gen(t * k + before), t, 2 * k, before, between)
     x[:, 7] = -100.0
     got, want = mx.quantize_mx(x, form, swiglu=True), mx.quantize_mx(x.contiguous().clone(), form, swiglu=True)
+    assert torch.equal(got[0].view(U8), want[0].view(U8)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("t,k", [(1, 128), (70, 512), (300, 2048)])
+def test_codes_as_activations_and_weights_at_once(t, k):
+    """The rows' products with each other: both operands are one memory."""
+    mx = lib()
+    q, s = mx.quantize_mx(randn(gen(t), t, k), "e2m1")
+    ref, mag = product((q, s), (q, s))
+    check(mx.linear_mx(q, s, q, s), ref, ref.abs() * 2.0 ** -8 + sum_bound(k, mag), "x times itself")
+
+
+@pytest.mark.parametrize("form", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("t,n", [(1, 32), (700, 2048), (5, 16416)])
+def test_norm_of_one_tensor_as_both_inputs(form, t, n):
+    """x as residual too, and the sum written over it."""
+    mx, g = lib(), gen(t)
+    x, w = randn(g, t, n), randn(g, n)
+    want = mx.residual_norm_mx(x, x.clone(), w, scale=0.5, format=form)
+    got = mx.residual_norm_mx(x, x, w, scale=0.5, format=form, residual_out=x)
+    assert got[2] is x and torch.equal(x, want[2])
     assert torch.equal(got[0].view(U8), want[0].view(U8)) and torch.equal(got[1], want[1])
